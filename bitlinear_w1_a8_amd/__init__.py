@@ -9,10 +9,17 @@ _EXPORTS = ("pack_weights", "quant_act", "subln_quant_act", "forward", "bitlinea
             "interleave_rows", "gated_relu2", "pack_weights_binary", "forward_binary",
             "gemv_max_tokens",
             "BitLinearError", "load", "last_error")
+_EXPERTS = ("Routing", "route_experts", "gated_relu2_experts", "linear_experts")
+_W4 = ("pack_weights_w4", "unpack_weights_w4", "forward_w4")
 
 
 def __getattr__(name):
     if name in _EXPORTS:
-        from . import binding
-        return getattr(binding, name)
-    raise AttributeError(name)
+        from . import binding as module
+    elif name in _EXPERTS:
+        from . import experts as module
+    elif name in _W4:
+        from . import w4 as module
+    else:
+        raise AttributeError(name)
+    return getattr(module, name)

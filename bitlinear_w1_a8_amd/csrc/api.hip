@@ -7,17 +7,14 @@
 #include "bitlinear.h"
 #include <cmath>
 
+#include "api_util.h"
 #include "bl_internal.h"
 
+namespace bl {
+
 namespace {
-
 thread_local std::string g_last_error;
-
-constexpr int64_t kMaxT = int64_t(1) << 24;
-constexpr int64_t kMaxN = int64_t(1) << 26;
-constexpr int64_t kMaxNK = int64_t(1) << 38;  // keeps every gamma bucket below 2^62
-constexpr int64_t kMaxTN = int64_t(1) << 36;  // y up to 256 GiB
-constexpr int64_t kMaxBinaryK = 32768;         // int8 rows of the binary decode kernel fit LDS
+}
 
 bl_status fail(bl_status code, const char* fmt, ...) {
   char buf[512];
@@ -29,28 +26,32 @@ bl_status fail(bl_status code, const char* fmt, ...) {
   return code;
 }
 
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-bl_status check_k(const char* fn, int64_t k) {
-  if (k < 16 || k > BITLINEAR_MAX_K || k % 16 != 0)
-    return fail(BL_ERR_SHAPE, "%s: K=%lld must be a multiple of 16 in [16, %d]", fn,
-                (long long)k, BITLINEAR_MAX_K);
-  return BL_OK;
-}
-
 bl_status launched(const char* fn, hipError_t e) {
   if (e != hipSuccess) return fail(BL_ERR_HIP, "%s: kernel launch failed: %s", fn, hipGetErrorString(e));
   g_last_error.clear();
   return BL_OK;
 }
 
-}  // namespace
+}  // namespace bl
+
+using bl::aligned;
+using bl::check_k;
+using bl::fail;
+using bl::kMaxN;
+using bl::kMaxNK;
+using bl::kMaxT;
+using bl::kMaxTN;
+using bl::launched;
+
+namespace {
+constexpr int64_t kMaxBinaryK = 32768;         // int8 rows of the binary decode kernel fit LDS
+}
 
 extern "C" {
 
 int bitlinear_abi_version(void) { return BITLINEAR_ABI_VERSION; }
 
-const char* bitlinear_last_error(void) { return g_last_error.c_str(); }
+const char* bitlinear_last_error(void) { return bl::g_last_error.c_str(); }
 
 int64_t bitlinear_gemv_max_tokens(void) { return bl::kGemvMaxTokens; }
 
