@@ -22,4 +22,5 @@ def __getattr__(name):
         from . import w4 as module
     else:
         raise AttributeError(name)
-    return getattr(module, name)
+    value = globals()[name] = getattr(module, name)   # found at once from now on
+    return value

@@ -7,7 +7,6 @@ Every step of the forward runs in the library's HIP kernels; there is no
 other code path.  If the library is not built, loading raises ImportError.
 """
 
-import contextlib
 import ctypes
 import os
 
@@ -93,17 +92,6 @@ def declare(signatures):
         fn.restype = res
         fn.argtypes = args
     return lib
-
-
-_here = contextlib.nullcontext()
-
-
-def on_device(device):
-    """Context in which `device` is the current one: a kernel can only be
-    launched on a stream of the current device."""
-    if device.index is None or device.index == torch.cuda.current_device():
-        return _here
-    return torch.cuda.device(device)
 
 
 def last_error():

@@ -16,7 +16,83 @@ hipError_t launch_route(const void* logits, int bf16, int64_t t, int64_t e, int6
                         int32_t* ids, float* weights, int32_t* offsets, int32_t* pairs,
                         int32_t* slots, int32_t* workspace, hipStream_t stream);
 
-// ---------------------------------------------------------------- experts (experts.hip)
+// ---------------------------------------------------------------- ragged rows
+
+// The routing as the kernels take it.
+struct Slots {
+  const int32_t* offsets;
+  const int32_t* pairs;
+  int E, P;
+  int k;                  // pairs / k is the row of x; 0: x has one row per slot
+};
+
+__device__ __forceinline__ int slot_row(const Slots& s, int p) {
+  if (s.k == 0) return p;
+  const int pair = min(max(s.pairs[p], 0), s.P - 1);
+  return (int)((uint32_t)pair / (uint32_t)s.k);
+}
+
+// Block `c` of `rows` slots each, counted over the experts in order: its
+// expert and slots p0 .. p1 - 1 (all in [0, P)), or false when there are
+// fewer.  Called by whole waves, with the same result in each.
+__device__ __forceinline__ bool find_rows(const Slots& s, int c, int rows, int& expert, int& p0,
+                                          int& p1) {
+  const int lane = threadIdx.x & 63;
+  int seen = 0;
+  for (int base = 0; base < s.E; base += 64) {
+    const int e = base + lane;
+    int lo = 0, hi = 0;
+    if (e < s.E) {
+      lo = min(max(s.offsets[e], 0), s.P);
+      hi = min(max(s.offsets[e + 1], lo), s.P);
+    }
+    const int n = (hi - lo + rows - 1) / rows;
+    int sum = n;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int o = __shfl_up(sum, d);
+      if (lane >= d) sum += o;
+    }
+    const int total = __builtin_amdgcn_readlane(sum, 63);
+    if (c < seen + total) {
+      const int at = __builtin_ctzll(__ballot(seen + sum > c));
+      const int first = __builtin_amdgcn_readlane(seen + sum - n, at);
+      lo = __builtin_amdgcn_readlane(lo, at);
+      hi = __builtin_amdgcn_readlane(hi, at);
+      expert = base + at;
+      p0 = lo + (c - first) * rows;
+      p1 = min(p0 + rows, hi);
+      return true;
+    }
+    seen += total;
+  }
+  return false;
+}
+
+// Row blocks of `rows` slots that P slots over E experts can make at most.
+inline int64_t row_blocks(int64_t p, int64_t e, int64_t rows) {
+  const int64_t most = p / rows + (p < e ? p : e);
+  return most < p ? most : p;
+}
+
+// Row blocks of `rows` slots that the experts make together (whole waves).
+__device__ __forceinline__ int count_row_blocks(const Slots& s, int rows) {
+  int n = 0;
+  for (int e = threadIdx.x & 63; e < s.E; e += 64) {
+    const int lo = min(max(s.offsets[e], 0), s.P), hi = min(max(s.offsets[e + 1], lo), s.P);
+    n += (hi - lo + rows - 1) / rows;
+  }
+  return wave_sum_i(n);
+}
+
+// ---------------------------------------------------------------- experts (experts.hip, gemm.hip)
+
+// The tiled MFMA kernel over each expert's rows: y (or, gated, h) by slot.
+// K % 64 == 0, rows of x times K below 2^31, N * K / 16 below 2^31.
+hipError_t launch_gemm_experts(const Slots& s, const uint8_t* packed, const float* gamma,
+                               const float* gamma2, const int8_t* xq, const float* absmax,
+                               int64_t n, int64_t k, float* y, uint16_t* h, int32_t* acc,
+                               hipStream_t stream);
 
 hipError_t launch_gated_experts(const bl_routing& r, const void* x, int bf16, const uint8_t* packed,
                                 const float* gamma_gate, const float* gamma_up, int64_t n,

@@ -25,6 +25,7 @@
 #include <type_traits>
 
 #include "bl_internal.h"
+#include "experts.h"
 
 namespace bl {
 namespace {
@@ -271,8 +272,11 @@ __device__ __align__(16) int8_t kZeroPage[1024];
 // past K are read from a page of zeros and its weight loads past the row end
 // reload the step's first half (multiplied by those zeros).  With K in parts
 // the half step falls in the last part.
+// EXPERTS: routed rows.  A row block holds slots of one expert; the block
+// finds them and the expert's matrix and gammas from the routing, gathers its
+// activation rows through it and writes by slot.  T is not used.
 template <int WAVES, int WAVES_M, int WMF, int WNF, int STAGES, bool SPLIT, bool GATED,
-          int WBITS = 2, bool RS = false, bool TAIL = false>
+          int WBITS = 2, bool RS = false, bool TAIL = false, bool EXPERTS = false>
 __global__ __launch_bounds__(WAVES * 64) void k_gemm_lds(const uint32_t* __restrict__ packed,
                                                          const float* __restrict__ gamma,
                                                          const int8_t* __restrict__ xq,
@@ -283,11 +287,13 @@ __global__ __launch_bounds__(WAVES * 64) void k_gemm_lds(const uint32_t* __restr
                                                          int ksteps, int splits,
                                                          const float* __restrict__ gamma2,
                                                          uint16_t* __restrict__ h_out,
-                                                         const int32_t* __restrict__ rowsum) {
+                                                         const int32_t* __restrict__ rowsum,
+                                                         const Slots slots) {
   static_assert(STAGES >= 2 && STAGES <= 4, "two to four stages");
   static_assert(!(RS && (GATED || WBITS != 2)), "rowsum: plain two-bit kernels only");
   static_assert(!(SPLIT && GATED), "the gated epilogue needs whole sums");
-  static_assert(!(TAIL && (GATED || WBITS != 2)), "a half last K step: plain two-bit kernels");
+  static_assert(!(TAIL && WBITS != 2), "a half last K step: two-bit kernels");
+  static_assert(!(EXPERTS && (SPLIT || RS || WBITS != 2)), "experts: whole sums of two-bit weights");
   constexpr int NT = WAVES * 64;
   constexpr int WAVES_N = WAVES / WAVES_M;
   constexpr int BM = WAVES_M * 32 * WMF, BN = WAVES_N * 32 * WNF;
@@ -343,13 +349,22 @@ __global__ __launch_bounds__(WAVES * 64) void k_gemm_lds(const uint32_t* __restr
   const int wm = wave / WAVES_N, wn = wave % WAVES_N;
   const int KW = K >> (WBITS == 2 ? 4 : 5);   // packed words per row
 
-  const int ntn = (N + BN - 1) / BN, ntm = (T + BM - 1) / BM;
+  const int ntn = (N + BN - 1) / BN;
+  const int ntm = EXPERTS ? count_row_blocks(slots, BM) : (T + BM - 1) / BM;
   const int tiles = ntn * ntm;
   // work item = (K part, tile); items next to each other share a K part, so
   // the blocks that run together share activation rows and weight columns
   const int items = SPLIT ? tiles * splits : tiles;
   int item = blockIdx.x;
-  if (items >= 8 && (items % 8) == 0) item = (blockIdx.x % 8) * (items / 8) + blockIdx.x / 8;
+  if constexpr (EXPERTS) {
+    // the grid covers the most tiles there can be: the tiles that there are
+    // go in equal runs to the XCDs
+    const int per_xcd = (items + 7) / 8, at = blockIdx.x / 8;
+    item = (blockIdx.x % 8) * per_xcd + at;
+    if (at >= per_xcd || item >= items) return;
+  } else {
+    if (items >= 8 && (items % 8) == 0) item = (blockIdx.x % 8) * (items / 8) + blockIdx.x / 8;
+  }
   const int part = SPLIT ? item / tiles : 0, tile = item - part * tiles;
   // grouped order: BL_GEMM_GROUP_M row blocks at a time, down the rows first,
   // so that the contiguous range of tiles one XCD runs covers a squarer block
@@ -358,7 +373,17 @@ __global__ __launch_bounds__(WAVES * 64) void k_gemm_lds(const uint32_t* __restr
   const int gid = tile / in_group, first_m = gid * BL_GEMM_GROUP_M;
   const int gsize = min(ntm - first_m, BL_GEMM_GROUP_M);
   const int r_in = tile - gid * in_group;
-  const int m0 = (first_m + r_in % gsize) * BM, n0 = (r_in / gsize) * BN;
+  const int n0 = (r_in / gsize) * BN;
+  int m0 = (first_m + r_in % gsize) * BM, mend = T;   // rows m0 .. mend - 1
+  if constexpr (EXPERTS) {
+    int expert = 0;
+    if (!find_rows(slots, first_m + r_in % gsize, BM, expert, m0, mend)) return;
+    packed += (int64_t)expert * N * KW;
+    gamma += expert;
+    if constexpr (GATED) gamma2 += expert;
+  }
+  // the activation row of output row `tok`
+  auto row_of = [&](int tok) { return EXPERTS ? slot_row(slots, tok) : tok; };
   const uint32_t kbase = (uint32_t)part * (uint32_t)ksteps * BK;   // first k of this part
 
   // per-token output scale first: its loads retire before the pipeline starts
@@ -368,15 +393,15 @@ __global__ __launch_bounds__(WAVES * 64) void k_gemm_lds(const uint32_t* __restr
       const float g2 = gamma2[0];
       for (int r = tid; r < BM; r += NT) {
         const int tok = m0 + r;
-        const float a = tok < T ? absmax[tok] : 0.0f;
+        const float a = tok < mend ? absmax[row_of(tok)] : 0.0f;
         gm_gate[r] = gamma_m(g, a);
         gm_up[r] = gamma_m(g2, a);
       }
     } else {
       for (int r = tid; r < BM; r += NT) {
         const int tok = m0 + r;
-        scale[r] = tok < T ? out_scale(g, absmax[tok]) : 0.0f;
-        if constexpr (RS) rsum[r] = tok < T && part == 0 ? rowsum[tok] : 0;
+        scale[r] = tok < mend ? out_scale(g, absmax[row_of(tok)]) : 0.0f;
+        if constexpr (RS) rsum[r] = tok < mend && part == 0 ? rowsum[tok] : 0;
       }
     }
   }
@@ -390,7 +415,7 @@ __global__ __launch_bounds__(WAVES * 64) void k_gemm_lds(const uint32_t* __restr
     const int r = 8 * c + (lane >> 3);
     const int slot = (lane & 7) ^ ((r >> 1) & 7);
     int tok = m0 + r;
-    tok = tok < T ? tok : T - 1;
+    tok = row_of(tok < mend ? tok : mend - 1);
     aoff[i] = (uint32_t)tok * (uint32_t)K + 16u * slot;
     aslot[i] = 16u * slot;
   }
@@ -611,7 +636,7 @@ __global__ __launch_bounds__(WAVES * 64) void k_gemm_lds(const uint32_t* __restr
           const int sv = exact_sum<WBITS>(acc[i][j][v], qs);
           // every lane takes part: lane l gets lane l ^ 1's sum
           const int other = __builtin_amdgcn_update_dpp(0, sv, 0xB1, 0xF, 0xF, false);
-          if (tok >= T || n >= N) continue;
+          if (tok >= mend || n >= N) continue;
           const int64_t o = (int64_t)tok * N + n;
           if (acc_out) acc_out[o] = sv;
           if ((m & 1) == 0)
@@ -627,7 +652,7 @@ __global__ __launch_bounds__(WAVES * 64) void k_gemm_lds(const uint32_t* __restr
     for (int v = 0; v < 16; ++v) {
       const int r = wm * 32 * WMF + i * 32 + (v >> 2) * 8 + h * 4 + (v & 3);
       const int tok = m0 + r;
-      if (tok >= T) continue;
+      if (tok >= mend) continue;
       const float sc = scale[r];
       const int qs = rsum[r];
 #pragma unroll
@@ -704,7 +729,7 @@ hipError_t run_lds(const uint8_t* packed, const float* gamma, const int8_t* xq,
   auto kern = pick();
   kern<<<dim3((unsigned)(tiles * splits)), WAVES * 64, 0, stream>>>(
       reinterpret_cast<const uint32_t*>(packed), gamma, xq, absmax, (int)t, (int)n, (int)k, y, acc,
-      ksteps, splits, gamma2, h, rowsum);
+      ksteps, splits, gamma2, h, rowsum, Slots{});
   return hipGetLastError();
 }
 
@@ -937,6 +962,55 @@ hipError_t launch_gemm_binary(const uint8_t* packed, const float* gamma, const i
       return run_lds<4, 1, 2, 2, BL_GEMM_STAGES, false, 1>(packed, gamma, xq, absmax, t, n, k, y,
                                                            acc, stream);
   }
+}
+
+namespace {
+
+template <int WAVES, int WAVES_M, int WMF, int WNF, int STAGES, bool GATED>
+hipError_t run_experts(const Slots& s, const uint8_t* packed, const float* gamma,
+                       const float* gamma2, const int8_t* xq, const float* absmax, int64_t n,
+                       int64_t k, float* y, uint16_t* h, int32_t* acc, hipStream_t stream) {
+  constexpr int BM = WAVES_M * 32 * WMF, BN = (WAVES / WAVES_M) * 32 * WNF;
+  const int64_t tiles = ((n + BN - 1) / BN) * row_blocks(s.P, s.E, BM);
+  auto kern = k % BK != 0
+                  ? k_gemm_lds<WAVES, WAVES_M, WMF, WNF, STAGES, false, GATED, 2, false, true, true>
+                  : k_gemm_lds<WAVES, WAVES_M, WMF, WNF, STAGES, false, GATED, 2, false, false, true>;
+  kern<<<dim3((unsigned)((tiles + 7) / 8 * 8)), WAVES * 64, 0, stream>>>(
+      reinterpret_cast<const uint32_t*>(packed), gamma, xq, absmax, 0, (int)n, (int)k, y, acc,
+      (int)(k / BK), 1, gamma2, h, nullptr, s);
+  return hipGetLastError();
+}
+
+// Tiles by the slots per expert, were all alike (row blocks are cut per
+// expert, so taller tiles leave more rows empty).  Gated, 64 experts of 2560 ->
+// 2 x 1024, 32 / 64 / 128 / 256 slots each: 64 x 256 tiles 43.3 / 61.0 / 86.3
+// / 128.0 us, 32 x 256 41.0 / 60.1 / 90.5 / 145.1, 32 x 128 41.7 / 64.8 /
+// 101.9 / 169.7 (128-row tiles at 256 slots: 145-158).  Narrow tiles
+// where the wide ones would not give each CU a few blocks (8 experts of 2560 ->
+// 2 x 1728, 16 / 32 slots each: 32 x 128 17.2 / 18.6 us, 32 x 256 18.7 / 19.4).
+template <bool GATED>
+hipError_t tile_experts(const Slots& s, const uint8_t* packed, const float* gamma,
+                        const float* gamma2, const int8_t* xq, const float* absmax, int64_t n,
+                        int64_t k, float* y, uint16_t* h, int32_t* acc, hipStream_t stream) {
+  const int64_t each = s.P / std::min(s.P, s.E), hit = std::min(s.P, s.E);
+  if (each >= 96)
+    return run_experts<4, 1, 2, 2, 3, GATED>(s, packed, gamma, gamma2, xq, absmax, n, k, y, h, acc,
+                                             stream);
+  if (hit * ((each + 31) / 32) * ((n + 255) / 256) >= 2 * device_cus())
+    return run_experts<4, 1, 1, 2, 3, GATED>(s, packed, gamma, gamma2, xq, absmax, n, k, y, h, acc,
+                                             stream);
+  return run_experts<4, 1, 1, 1, 4, GATED>(s, packed, gamma, gamma2, xq, absmax, n, k, y, h, acc,
+                                           stream);
+}
+
+}  // namespace
+
+hipError_t launch_gemm_experts(const Slots& s, const uint8_t* packed, const float* gamma,
+                               const float* gamma2, const int8_t* xq, const float* absmax,
+                               int64_t n, int64_t k, float* y, uint16_t* h, int32_t* acc,
+                               hipStream_t stream) {
+  return h ? tile_experts<true>(s, packed, gamma, gamma2, xq, absmax, n, k, y, h, acc, stream)
+           : tile_experts<false>(s, packed, gamma, gamma2, xq, absmax, n, k, y, h, acc, stream);
 }
 
 }  // namespace bl

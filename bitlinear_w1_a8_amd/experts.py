@@ -6,13 +6,13 @@ the caller's device and every step runs in the library's HIP kernels on the
 current stream of that device.
 """
 
-import ctypes
+import struct
 
 import torch
 
 from . import binding
-from .binding import (BL_BF16, BL_F32, _c_i64, _c_int, _c_sz, _c_vp, _check, _need_cuda, _need_shape,
-                      _ptr, _same_device, _stream)
+from ._marshal import call, device_of, need
+from .binding import BL_BF16, BL_F32, _c_i64, _c_int, _c_sz, _c_vp
 
 #: most experts and most experts per token that the library takes
 MAX_EXPERTS, MAX_TOP_K = 1024, 32
@@ -22,23 +22,18 @@ _TOKENS, _SLOTS = 0, 1                       # bl_rows
 _DTYPES = {torch.float32: BL_F32, torch.bfloat16: BL_BF16}
 
 
-class BlRouting(ctypes.Structure):
-    """struct bl_routing of include/bitlinear_experts.h."""
-    _fields_ = [("T", _c_i64), ("k", _c_i64), ("E", _c_i64), ("offsets", _c_vp), ("pairs", _c_vp),
-                ("slots", _c_vp), ("weights", _c_vp)]
-
-
-_ROUTING = ctypes.POINTER(BlRouting)
+#: struct bl_routing: T, k, E, then the pointers offsets, pairs, slots, weights
+_ROUTING = struct.Struct("=7q")
 
 # name -> (restype, argtypes), as declared in include/bitlinear_experts.h
 SIGNATURES = {
     "bitlinear_route_workspace_bytes": (_c_sz, [_c_i64, _c_i64]),
     "bitlinear_route_experts": (_c_int, [_c_vp, _c_int, _c_i64, _c_i64, _c_i64, _c_int, _c_vp, _c_vp,
                                          _c_vp, _c_vp, _c_vp, _c_vp, _c_sz, _c_vp]),
-    "bitlinear_gated_relu2_experts": (_c_int, [_ROUTING, _c_vp, _c_int, _c_vp, _c_vp, _c_vp, _c_i64,
+    "bitlinear_gated_relu2_experts": (_c_int, [_c_vp, _c_vp, _c_int, _c_vp, _c_vp, _c_vp, _c_i64,
                                                _c_i64, _c_vp, _c_vp, _c_vp, _c_vp, _c_vp]),
     "bitlinear_experts_workspace_bytes": (_c_sz, [_c_i64, _c_i64, _c_i64]),
-    "bitlinear_linear_experts": (_c_int, [_ROUTING, _c_vp, _c_int, _c_int, _c_vp, _c_vp, _c_i64,
+    "bitlinear_linear_experts": (_c_int, [_c_vp, _c_vp, _c_int, _c_int, _c_vp, _c_vp, _c_i64,
                                           _c_i64, _c_vp, _c_int, _c_vp, _c_vp, _c_vp, _c_vp, _c_sz,
                                           _c_vp]),
 }
@@ -69,21 +64,20 @@ class Routing:
     def __init__(self, ids, weights, offsets, pairs, slots):
         self.ids, self.weights, self.offsets, self.pairs, self.slots = ids, weights, offsets, pairs, slots
 
-    def _struct(self, name, x):
+    def _struct(self, dev):
         """Checked against the shapes that the library reads, and as its struct."""
-        if self.slots.dim() != 2:
+        slots, offsets = self.slots, self.offsets
+        if slots.dim() != 2:
             raise ValueError("routing.slots must be [T, k]")
-        t, k = self.slots.shape
-        e = self.offsets.numel() - 1
-        for field in ("offsets", "pairs", "slots"):
-            _need_cuda(getattr(self, field), f"routing.{field}", torch.int32)
-        _need_cuda(self.weights, "routing.weights", torch.float32)
-        _need_shape(self.offsets, "routing.offsets", (e + 1,))
-        _need_shape(self.pairs, "routing.pairs", (t * k,))
-        _need_shape(self.weights, "routing.weights", (t, k))
-        _same_device(name, x, self.offsets, self.pairs, self.slots, self.weights)
-        return t, k, e, BlRouting(t, k, e, self.offsets.data_ptr(), self.pairs.data_ptr(),
-                                  self.slots.data_ptr(), self.weights.data_ptr())
+        shape = slots.shape
+        t, k = shape
+        e = offsets.numel() - 1
+        need(dev, slots, "routing.slots", torch.int32, shape)
+        need(dev, offsets, "routing.offsets", torch.int32, (e + 1,))
+        need(dev, self.pairs, "routing.pairs", torch.int32, (t * k,))
+        need(dev, self.weights, "routing.weights", torch.float32, shape)
+        return t, k, e, _ROUTING.pack(t, k, e, offsets.data_ptr(), self.pairs.data_ptr(),
+                                      slots.data_ptr(), self.weights.data_ptr())
 
 
 def route_experts(logits, k, share="chosen"):
@@ -91,7 +85,7 @@ def route_experts(logits, k, share="chosen"):
     token's k largest logits (ties to the lower expert; -inf and NaN never
     taken).  share: "chosen" (softmax over the chosen logits) or "all"."""
     lib = _load()
-    _need_cuda(logits, "logits")
+    dev = device_of(logits, "logits")
     dt = _DTYPES.get(logits.dtype)
     if dt is None:
         raise TypeError(f"logits must be float32 or bfloat16, got {logits.dtype}")
@@ -99,73 +93,81 @@ def route_experts(logits, k, share="chosen"):
         raise ValueError("logits must be [T, E]")
     if share not in SHARES:
         raise ValueError(f"share must be one of {sorted(SHARES)}, got {share!r}")
-    t, e = logits.shape
-    k, dev = int(k), logits.device
+    t, e = shape = logits.shape
+    need(dev, logits, "logits", logits.dtype, shape)
+    k = int(k)
     if k < 1:
         raise ValueError(f"k must be at least 1, got {k}")
-    ids = torch.empty((t, k), dtype=torch.int32, device=dev)
-    weights = torch.empty((t, k), dtype=torch.float32, device=dev)
-    offsets = torch.empty(e + 1, dtype=torch.int32, device=dev)
-    pairs = torch.empty(t * k, dtype=torch.int32, device=dev)
-    slots = torch.empty((t, k), dtype=torch.int32, device=dev)
+    on = logits.device
+    ids = torch.empty((t, k), dtype=torch.int32, device=on)
+    weights = torch.empty((t, k), dtype=torch.float32, device=on)
+    offsets = torch.empty(e + 1, dtype=torch.int32, device=on)
+    pairs = torch.empty(t * k, dtype=torch.int32, device=on)
+    slots = torch.empty((t, k), dtype=torch.int32, device=on)
     wsb = lib.bitlinear_route_workspace_bytes(t, e)
-    ws = torch.empty(wsb, dtype=torch.uint8, device=dev) if wsb else None
-    with binding.on_device(dev):
-        _check(lib.bitlinear_route_experts(_ptr(logits), dt, t, e, k, SHARES[share], _ptr(ids),
-                                           _ptr(weights), _ptr(offsets), _ptr(pairs), _ptr(slots),
-                                           _ptr(ws), wsb, _stream(dev)))
+    ws = torch.empty(wsb, dtype=torch.uint8, device=on) if wsb else None
+    call(dev, lib.bitlinear_route_experts, logits.data_ptr(), dt, t, e, k, SHARES[share],
+         ids.data_ptr(), weights.data_ptr(), offsets.data_ptr(), pairs.data_ptr(),
+         slots.data_ptr(), ws.data_ptr() if wsb else None, wsb)
     return Routing(ids, weights, offsets, pairs, slots)
 
 
-def _rows(x, name, rows, what):
-    _need_cuda(x, name)
+def _rows(dev, x, rows, what):
     dt = _DTYPES.get(x.dtype)
     if dt is None:
-        raise TypeError(f"{name} must be float32 or bfloat16, got {x.dtype}")
+        raise TypeError(f"x must be float32 or bfloat16, got {x.dtype}")
     if x.dim() != 2 or x.shape[0] != rows:
-        raise ValueError(f"{name} must have one row per {what}: [{rows}, K], got {tuple(x.shape)}")
-    return dt
+        raise ValueError(f"x must have one row per {what}: [{rows}, K], got {tuple(x.shape)}")
+    need(dev, x, "x", x.dtype, x.shape)
+    return dt, x.shape[1]
 
 
-def _out(out, name, shape, dtype, dev):
+def _out(dev, out, shape, dtype, on):
     if out is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
-    _need_cuda(out, name, dtype)
-    _need_shape(out, name, shape)
+        return torch.empty(shape, dtype=dtype, device=on)
+    need(dev, out, "out", dtype, shape)
     return out
 
 
-def gated_relu2_experts(x, packed_gu, gamma_gate, gamma_up, routing, want_acc=False, out=None):
+def _up(n):
+    return (n + 255) & ~255
+
+
+def gated_relu2_experts(x, packed_gu, gamma_gate, gamma_up, routing, want_codes=False,
+                        want_acc=False, out=None):
     """Gate and up projections of the routed tokens with the squared-ReLU gate.
 
     x [T, K] (float32 or bfloat16); packed_gu uint8 [E, 2N, K/4], each
     expert's rows from interleave_rows; gamma_gate, gamma_up float32 [E].
-    Returns (h bfloat16 [T * k, N] by slot, xq, absmax, acc int32 [T * k, 2N]
-    or None).  Rows of empty slots are not written: undefined, or with `out`
-    as they were."""
+    Returns (h bfloat16 [T * k, N] by slot, xq int8 [T, K] and absmax float32
+    [T] of the tokens with an expert or None without `want_codes`, acc int32
+    [T * k, 2N] or None without `want_acc`).  Rows of empty slots are not
+    written: undefined, or with `out` as they were."""
     lib = _load()
-    t, k, e, desc = routing._struct("gated_relu2_experts", x)
-    dt = _rows(x, "x", t, "token")
-    kk = x.shape[1]
-    _need_cuda(packed_gu, "packed_gu", torch.uint8)
-    _need_cuda(gamma_gate, "gamma_gate", torch.float32)
-    _need_cuda(gamma_up, "gamma_up", torch.float32)
+    dev = device_of(x, "x")
+    t, k, e, desc = routing._struct(dev)
+    dt, kk = _rows(dev, x, t, "token")
     if packed_gu.dim() != 3 or packed_gu.shape[1] % 2:
         raise ValueError("packed_gu must be [E, 2N, K/4]")
     n = packed_gu.shape[1] // 2
-    _need_shape(packed_gu, "packed_gu", (e, 2 * n, kk // 4))
-    _need_shape(gamma_gate, "gamma_gate", (e,))
-    _need_shape(gamma_up, "gamma_up", (e,))
-    dev = x.device
-    h = _out(out, "out", (t * k, n), torch.bfloat16, dev)
-    _same_device("gated_relu2_experts", x, packed_gu, gamma_gate, gamma_up, h)
-    xq = torch.empty((t, kk), dtype=torch.int8, device=dev)
-    absmax = torch.empty(t, dtype=torch.float32, device=dev)
-    acc = torch.empty((t * k, 2 * n), dtype=torch.int32, device=dev) if want_acc else None
-    with binding.on_device(dev):
-        _check(lib.bitlinear_gated_relu2_experts(ctypes.byref(desc), _ptr(x), dt, _ptr(packed_gu),
-                                                 _ptr(gamma_gate), _ptr(gamma_up), n, kk, _ptr(h),
-                                                 _ptr(xq), _ptr(absmax), _ptr(acc), _stream(dev)))
+    need(dev, packed_gu, "packed_gu", torch.uint8, (e, 2 * n, kk // 4))
+    need(dev, gamma_gate, "gamma_gate", torch.float32, (e,))
+    need(dev, gamma_up, "gamma_up", torch.float32, (e,))
+    on = x.device
+    h = _out(dev, out, (t * k, n), torch.bfloat16, on)
+    if want_codes:
+        xq = torch.empty((t, kk), dtype=torch.int8, device=on)
+        absmax = torch.empty(t, dtype=torch.float32, device=on)
+        codes = xq.data_ptr(), absmax.data_ptr()
+    else:                       # scratch, in one piece
+        xq = absmax = None
+        scratch = torch.empty(_up(t * kk) + 4 * t, dtype=torch.uint8, device=on)
+        at = scratch.data_ptr()
+        codes = at, at + _up(t * kk)
+    acc = torch.empty((t * k, 2 * n), dtype=torch.int32, device=on) if want_acc else None
+    call(dev, lib.bitlinear_gated_relu2_experts, desc, x.data_ptr(), dt, packed_gu.data_ptr(),
+         gamma_gate.data_ptr(), gamma_up.data_ptr(), n, kk, h.data_ptr(), *codes,
+         acc.data_ptr() if want_acc else None)
     return h, xq, absmax, acc
 
 
@@ -179,34 +181,29 @@ def linear_experts(x, packed, gamma, routing, combine=True, x_rows="slots", want
     row per slot, [T * k, N], rows of empty slots not written (undefined, or
     with `out` as they were), and (y, acc int32) if want_acc."""
     lib = _load()
-    t, k, e, desc = routing._struct("linear_experts", x)
+    dev = device_of(x, "x")
+    t, k, e, desc = routing._struct(dev)
     if x_rows not in ("slots", "tokens"):
         raise ValueError(f"x_rows must be 'slots' or 'tokens', got {x_rows!r}")
     if combine and want_acc:
         raise ValueError("want_acc: the sums are per slot (combine=False only)")
     by_slot = x_rows == "slots"
     rows = t * k if by_slot else t
-    dt = _rows(x, "x", rows, "slot" if by_slot else "token")
-    kk = x.shape[1]
-    _need_cuda(packed, "packed", torch.uint8)
-    _need_cuda(gamma, "gamma", torch.float32)
+    dt, kk = _rows(dev, x, rows, "slot" if by_slot else "token")
     if packed.dim() != 3:
         raise ValueError("packed must be [E, N, K/4]")
     n = packed.shape[1]
-    _need_shape(packed, "packed", (e, n, kk // 4))
-    _need_shape(gamma, "gamma", (e,))
-    dev = x.device
-    y = _out(out, "out", (t if combine else t * k, n), torch.float32, dev)
-    _same_device("linear_experts", x, packed, gamma, y)
-    xq = torch.empty((rows, kk), dtype=torch.int8, device=dev)
-    absmax = torch.empty(rows, dtype=torch.float32, device=dev)
-    acc = torch.empty((t * k, n), dtype=torch.int32, device=dev) if want_acc else None
+    need(dev, packed, "packed", torch.uint8, (e, n, kk // 4))
+    need(dev, gamma, "gamma", torch.float32, (e,))
+    on = x.device
+    y = _out(dev, out, (t if combine else t * k, n), torch.float32, on)
+    acc = torch.empty((t * k, n), dtype=torch.int32, device=on) if want_acc else None
+    # the int8 rows, their absmax and the slots' rows, in one piece
     wsb = lib.bitlinear_experts_workspace_bytes(t, k, n) if combine else 0
-    ws = torch.empty(wsb, dtype=torch.uint8, device=dev) if combine else None
-    with binding.on_device(dev):
-        _check(lib.bitlinear_linear_experts(ctypes.byref(desc), _ptr(x), dt,
-                                            _SLOTS if by_slot else _TOKENS, _ptr(packed),
-                                            _ptr(gamma), n, kk, _ptr(y),
-                                            _TOKENS if combine else _SLOTS, _ptr(xq),
-                                            _ptr(absmax), _ptr(acc), _ptr(ws), wsb, _stream(dev)))
+    a, b = _up(rows * kk), _up(4 * rows)
+    scratch = torch.empty(a + b + wsb, dtype=torch.uint8, device=on)
+    at = scratch.data_ptr()
+    call(dev, lib.bitlinear_linear_experts, desc, x.data_ptr(), dt, _SLOTS if by_slot else _TOKENS,
+         packed.data_ptr(), gamma.data_ptr(), n, kk, y.data_ptr(), _TOKENS if combine else _SLOTS,
+         at, at + a, acc.data_ptr() if want_acc else None, at + a + b if combine else None, wsb)
     return (y, acc) if want_acc else y

@@ -5,8 +5,8 @@ step A1's int8 tokens.  Argument marshalling only, as ``binding``."""
 import torch
 
 from . import binding
-from .binding import (_c_i64, _c_int, _c_vp, _check, _need_cuda, _need_shape, _ptr, _same_device,
-                      _stream)
+from ._marshal import call, device_of, need
+from .binding import _c_i64, _c_int, _c_vp
 
 # name -> (restype, argtypes), as declared in include/bitlinear_w4.h
 SIGNATURES = {
@@ -28,19 +28,17 @@ def _load():
     return _lib
 
 
-def _matrix(packed, scales, zeros, k):
+def _matrix(dev, packed, scales, zeros, k):
     """Checks a packed matrix of rows of k weights; returns (rows, group)."""
-    _need_cuda(packed, "packed", torch.uint8)
-    _need_cuda(scales, "scales", torch.bfloat16)
-    if packed.dim() != 2 or scales.dim() != 2 or scales.shape[0] != packed.shape[0]:
+    if packed.dim() != 2 or scales.dim() != 2:
         raise ValueError("packed must be [N, row bytes] and scales [N, K/G]")
-    n, groups = scales.shape
+    n, groups = shape = scales.shape
     if groups < 1 or k % groups:
         raise ValueError(f"scales of {groups} groups do not cut rows of {k} weights evenly")
-    _need_shape(packed, "packed", (n, (k + 127) // 128 * 64))
+    need(dev, scales, "scales", torch.bfloat16, shape)
+    need(dev, packed, "packed", torch.uint8, (n, (k + 127) // 128 * 64))
     if zeros is not None:
-        _need_cuda(zeros, "zeros", torch.int8)
-        _need_shape(zeros, "zeros", (n, groups))
+        need(dev, zeros, "zeros", torch.int8, shape)
     return n, k // groups
 
 
@@ -49,33 +47,30 @@ def pack_weights_w4(w, group=128, with_zeros=False):
     bfloat16 [N, K / group], zeros int8 [N, K / group] or None); group 32, 64
     or 128."""
     lib = _load()
-    _need_cuda(w, "w", torch.float32)
+    dev = device_of(w, "w")
     if w.dim() != 2:
         raise ValueError("w must be [N, K]")
-    n, k = w.shape
-    group, dev = int(group), w.device
+    n, k = shape = w.shape
+    need(dev, w, "w", torch.float32, shape)
+    group, on = int(group), w.device
     if group not in (32, 64, 128) or k % group:
         raise ValueError(f"group must be 32, 64 or 128 and divide K={k}, got {group}")
-    packed = torch.empty((n, (k + 127) // 128 * 64), dtype=torch.uint8, device=dev)
-    scales = torch.empty((n, k // group), dtype=torch.bfloat16, device=dev)
-    zeros = torch.empty((n, k // group), dtype=torch.int8, device=dev) if with_zeros else None
-    with binding.on_device(dev):
-        _check(lib.bitlinear_pack_weights_w4(_ptr(w), n, k, group, _ptr(packed), _ptr(scales),
-                                             _ptr(zeros), _stream(dev)))
+    packed = torch.empty((n, (k + 127) // 128 * 64), dtype=torch.uint8, device=on)
+    scales = torch.empty((n, k // group), dtype=torch.bfloat16, device=on)
+    zeros = torch.empty((n, k // group), dtype=torch.int8, device=on) if with_zeros else None
+    call(dev, lib.bitlinear_pack_weights_w4, w.data_ptr(), n, k, group, packed.data_ptr(),
+         scales.data_ptr(), zeros.data_ptr() if with_zeros else None)
     return packed, scales, zeros
 
 
 def unpack_weights_w4(packed, scales, zeros, k):
     """The float32 values [N, k] that a packed matrix stands for."""
     lib = _load()
-    k = int(k)
-    n, group = _matrix(packed, scales, zeros, k)
-    _same_device("unpack_weights_w4", packed, scales, zeros)
-    dev = packed.device
-    w = torch.empty((n, k), dtype=torch.float32, device=dev)
-    with binding.on_device(dev):
-        _check(lib.bitlinear_unpack_weights_w4(_ptr(packed), _ptr(scales), _ptr(zeros), n, k, group,
-                                               _ptr(w), _stream(dev)))
+    k, dev = int(k), device_of(packed, "packed")
+    n, group = _matrix(dev, packed, scales, zeros, k)
+    w = torch.empty((n, k), dtype=torch.float32, device=packed.device)
+    call(dev, lib.bitlinear_unpack_weights_w4, packed.data_ptr(), scales.data_ptr(),
+         None if zeros is None else zeros.data_ptr(), n, k, group, w.data_ptr())
     return w
 
 
@@ -83,22 +78,18 @@ def forward_w4(packed, scales, xq, absmax, zeros=None, out=None):
     """y float32 [T, N] = tokens of step A1 (xq int8 [T, K], absmax float32
     [T], from quant_act or subln_quant_act) times a 4-bit matrix."""
     lib = _load()
-    _need_cuda(xq, "xq", torch.int8)
-    _need_cuda(absmax, "absmax", torch.float32)
+    dev = device_of(xq, "xq")
     if xq.dim() != 2:
         raise ValueError("xq must be [T, K]")
-    t, k = xq.shape
-    n, group = _matrix(packed, scales, zeros, k)
-    _need_shape(absmax, "absmax", (t,))
-    dev = xq.device
+    t, k = shape = xq.shape
+    need(dev, xq, "xq", torch.int8, shape)
+    n, group = _matrix(dev, packed, scales, zeros, k)
+    need(dev, absmax, "absmax", torch.float32, (t,))
     if out is None:
-        y = torch.empty((t, n), dtype=torch.float32, device=dev)
+        out = torch.empty((t, n), dtype=torch.float32, device=xq.device)
     else:
-        _need_cuda(out, "out", torch.float32)
-        _need_shape(out, "out", (t, n))
-        y = out
-    _same_device("forward_w4", packed, scales, zeros, xq, absmax, y)
-    with binding.on_device(dev):
-        _check(lib.bitlinear_forward_w4(_ptr(packed), _ptr(scales), _ptr(zeros), _ptr(xq),
-                                        _ptr(absmax), t, n, k, group, _ptr(y), _stream(dev)))
-    return y
+        need(dev, out, "out", torch.float32, (t, n))
+    call(dev, lib.bitlinear_forward_w4, packed.data_ptr(), scales.data_ptr(),
+         None if zeros is None else zeros.data_ptr(), xq.data_ptr(), absmax.data_ptr(), t, n, k,
+         group, out.data_ptr())
+    return out

@@ -96,7 +96,8 @@ bl_status bitlinear_route_experts(const void* logits, int dtype, int64_t T, int6
  *   h           [T * k, N] bfloat16 output (uint16 bit patterns), by slot; rows of
  *               empty slots are left as they were.
  *   xq          [T, K] int8 activations (written), 16-byte aligned.
- *   absmax      [T] token absmax (written), 4-byte aligned.
+ *   absmax      [T] token absmax (written), 4-byte aligned.  In both, rows of tokens
+ *               without an expert may be left as they were.
  *   acc         [T * k, 2N] exact int32 sums by slot, interleaved as the rows, or NULL.
  * Errors: BL_ERR_NULL, BL_ERR_SHAPE, BL_ERR_ALIGN, BL_ERR_DTYPE, BL_ERR_HIP. */
 bl_status bitlinear_gated_relu2_experts(const bl_routing* routing, const void* x, int x_dtype,
@@ -126,7 +127,8 @@ size_t bitlinear_experts_workspace_bytes(int64_t T, int64_t k, int64_t N);
  *              T * k * N <= 2^36.
  *   y          float32 output, 4-byte aligned.
  *   xq         int8 activations (written), as many rows as x, 16-byte aligned.
- *   absmax     row absmax (written), one per row of x, 4-byte aligned.
+ *   absmax     row absmax (written), one per row of x, 4-byte aligned.  In both, rows of
+ *              empty slots or of tokens without an expert may be left as they were.
  *   acc        [T * k, N] exact int32 sums by slot, or NULL (BL_ROWS_SLOTS outputs only).
  *   workspace  device scratch, 16-byte aligned, of at least
  *              bitlinear_experts_workspace_bytes(T, k, N) bytes with BL_ROWS_TOKENS

@@ -2,7 +2,6 @@
 symbols, binding signatures, and every refusal, made on the host before any
 HIP call.  Every call below fails at least one check; none reaches a launch."""
 
-import ctypes
 import os
 import re
 
@@ -80,14 +79,14 @@ def test_route_refusals(lib, kw, code):
 
 
 def _desc(t=4, k=2, e=8, offsets=A16, pairs=A16, slots=A16, weights=A16):
-    from bitlinear_w1_a8_amd.experts import BlRouting
-    return BlRouting(t, k, e, offsets, pairs, slots, weights)
+    from bitlinear_w1_a8_amd.experts import _ROUTING
+    return _ROUTING.pack(t, k, e, offsets or 0, pairs or 0, slots or 0, weights or 0)
 
 
 def _gated(lib, desc=None, x=A16, dt=1, packed=A16, g=A16, u=A16, n=16, k=64, h=A16, xq=A16,
            absmax=A16, acc=None):
     d = desc or _desc()
-    return lib.bitlinear_gated_relu2_experts(ctypes.byref(d), x, dt, packed, g, u, n, k, h, xq,
+    return lib.bitlinear_gated_relu2_experts(d, x, dt, packed, g, u, n, k, h, xq,
                                              absmax, acc, None)
 
 
@@ -120,7 +119,7 @@ def test_routing_refusals(lib):
 def _linear(lib, desc=None, x=A16, dt=1, xr=1, packed=A16, g=A16, n=16, k=64, y=A16, yr=0, xq=A16,
             absmax=A16, acc=None, ws=A16, wsb=BIG):
     d = desc or _desc()
-    return lib.bitlinear_linear_experts(ctypes.byref(d), x, dt, xr, packed, g, n, k, y, yr, xq, absmax,
+    return lib.bitlinear_linear_experts(d, x, dt, xr, packed, g, n, k, y, yr, xq, absmax,
                                         acc, ws, wsb, None)
 
 
