@@ -1,11 +1,35 @@
 // Internal declarations of the routed-expert and 4-bit operators.
 #pragma once
 
+#include <atomic>
+
 #include "bitlinear_experts.h"
 #include "bitlinear_w4.h"
 #include "bl_internal.h"
 
 namespace bl {
+
+constexpr int kMaxLds = 150 * 1024;   // dynamic LDS of a block (a CU has 160 KiB, the static part included)
+
+// A kernel that may ask for more dynamic LDS than the 64 KiB that a launch
+// gets without saying so; said once per kernel and device (saying it again,
+// as two threads may, does no harm).
+template <auto KERNEL>
+struct Kernel {
+  static constexpr auto kernel = KERNEL;
+  hipError_t allow_lds() const {
+    static std::atomic<uint64_t> set{0};
+    int dev = 0;
+    hipError_t e = hipGetDevice(&dev);
+    if (e != hipSuccess) return e;
+    const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+    if (set.load(std::memory_order_relaxed) & bit) return hipSuccess;
+    e = hipFuncSetAttribute(reinterpret_cast<const void*>(KERNEL),
+                            hipFuncAttributeMaxDynamicSharedMemorySize, kMaxLds);
+    if (e == hipSuccess) set.fetch_or(bit, std::memory_order_relaxed);
+    return e;
+  }
+};
 
 // ---------------------------------------------------------------- router (route.hip)
 

@@ -5,7 +5,6 @@
 // partly filled one), every block finds its expert and rows from the offsets,
 // and the blocks left over end at once.
 #include <algorithm>
-#include <atomic>
 #include <type_traits>
 
 #include "experts.h"
@@ -13,7 +12,6 @@
 namespace bl {
 namespace {
 
-constexpr int kMaxLds = 156 * 1024;   // dynamic LDS of a block (a CU has 160 KiB)
 
 // Batches whose step A1 is repeated by every block instead of launched on its
 // own.  Gated, 64 experts of 2560 -> 2 x 1024, 8 per token, on one card: T = 1
@@ -551,22 +549,6 @@ bool few_fits(int64_t k, int rows, int mode) {
   return k % 64 == 0 && few_lds(k, rows, mode) <= (size_t)kMaxLds;
 }
 
-// Dynamic LDS past the 64 KiB that a launch may ask for without saying so:
-// set once per kernel and device (setting it again is harmless).
-template <typename F>
-hipError_t allow_lds(F kern) {
-  static std::atomic<uint64_t> set{0};
-  int dev = 0;
-  hipError_t e = hipGetDevice(&dev);
-  if (e != hipSuccess) return e;
-  const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
-  if (bit && (set.load(std::memory_order_relaxed) & bit)) return hipSuccess;
-  e = hipFuncSetAttribute(reinterpret_cast<const void*>(kern),
-                          hipFuncAttributeMaxDynamicSharedMemorySize, kMaxLds);
-  if (e == hipSuccess) set.fetch_or(bit, std::memory_order_relaxed);
-  return e;
-}
-
 template <int MODE, bool GATED>
 hipError_t launch_few(const Slots& s, const uint8_t* packed, const float* gamma,
                       const float* gamma2, const void* x, const float* absmax, int64_t n,
@@ -579,17 +561,17 @@ hipError_t launch_few(const Slots& s, const uint8_t* packed, const float* gamma,
   const int64_t blocks = row_blocks(s.P, s.E, rows), bn = 16 * waves;
   const size_t lds = few_lds(k, rows, MODE);
   auto go = [&](auto kern) {
-    hipError_t e = allow_lds(kern);
+    hipError_t e = kern.allow_lds();
     for (int64_t b = 0; e == hipSuccess && b < blocks; b += 65535) {   // grid.y: at most 65535
       const dim3 grid((unsigned)((n + bn - 1) / bn), (unsigned)std::min<int64_t>(blocks - b, 65535));
-      kern<<<grid, 64 * waves, lds, stream>>>(s, w, gamma, gamma2, x, absmax, (int)n, (int)k, rows,
+      kern.kernel<<<grid, 64 * waves, lds, stream>>>(s, w, gamma, gamma2, x, absmax, (int)n, (int)k, rows,
                                               (int)b, y, h, acc, xq_out, absmax_out);
       e = hipGetLastError();
     }
     return e;
   };
-  if (k <= 1024) return go(k_experts_few<MODE, GATED, 4>);
-  return go(k_experts_few<MODE, GATED, 10>);
+  if (k <= 1024) return go(Kernel<k_experts_few<MODE, GATED, 4>>{});
+  return go(Kernel<k_experts_few<MODE, GATED, 10>>{});
 }
 
 template <int MODE>
@@ -601,14 +583,14 @@ hipError_t launch_token(const Slots& s, const bl_routing& r, const uint8_t* pack
   const dim3 grid((unsigned)((n + 15) / 16), (unsigned)r.T);
   const size_t lds = (size_t)topk * few_stride((int)k);
   auto go = [&](auto kern) {
-    hipError_t e = allow_lds(kern);
+    hipError_t e = kern.allow_lds();
     if (e != hipSuccess) return e;
-    kern<<<grid, 64 * topk * team, lds, stream>>>(s, r.slots, r.weights, topk, team,
+    kern.kernel<<<grid, 64 * topk * team, lds, stream>>>(s, r.slots, r.weights, topk, team,
                                                   reinterpret_cast<const uint32_t*>(packed), gamma,
                                                   x, (int)n, (int)k, y, xq, absmax);
     return hipGetLastError();
   };
-  return go(k_experts_token<MODE, 4>);
+  return go(Kernel<k_experts_token<MODE, 4>>{});
 }
 
 template <bool GATED>

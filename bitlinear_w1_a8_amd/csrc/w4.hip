@@ -5,10 +5,9 @@
 // int8: (w << 4) & 0xF0F0F0F0 and w & 0xF0F0F0F0 turn a packed word into eight
 // consecutive k of MFMA operand in three VALU operations, with no table and no
 // offset to take off.  The int8 MFMA sums a group exactly; the sum is converted
-// once per group and multiplied by the group's scale, 1/16 (a power of two)
-// and the token's absmax / 127 follow in the epilogue.  Zero points need the
-// group's sum of q as well, which one more MFMA against a matrix of ones
-// gives, in the same lanes as the products.
+// once per group and multiplied by the group's scale; 1/16 (a power of two)
+// and the token's absmax / 127 follow in the epilogue.  Zero points come off
+// the codes, five more operations per word, as t - z still fits an int8.
 //
 // The tokens are the rows (A) and the weights the columns (B) of the 16 x 16
 // result: every lane then works on one weight row, so it has one scale per
@@ -22,6 +21,7 @@ namespace bl {
 namespace {
 
 constexpr int kBlock = 128;      // weights per packed block (64 bytes)
+typedef float v16f __attribute__((ext_vector_type(16)));
 
 __device__ __forceinline__ float bf16_f(uint16_t b) { return __uint_as_float((uint32_t)b << 16); }
 __device__ __forceinline__ uint16_t f_bf16(float f) {   // finite f >= 0, nearest even
@@ -138,87 +138,449 @@ __global__ __launch_bounds__(256) void k_unpack_w4(const uint4* __restrict__ pac
 
 // ------------------------------------------------------------------ product
 
-// Up to 16 tokens and 16 weight rows per block; the waves take the blocks of
-// 128 k in turn and add their sums through LDS in order.
-template <int G, bool ZEROS>
-__global__ __launch_bounds__(256) void k_w4_rows(const uint4* __restrict__ packed,
-                                                 const uint16_t* __restrict__ scales,
-                                                 const int8_t* __restrict__ zeros,
-                                                 const int8_t* __restrict__ xq,
-                                                 const float* __restrict__ absmax, int T, int N,
-                                                 int K, float* __restrict__ y) {
-  constexpr int kWaves = 4;
-  __shared__ float red[kWaves][4][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int q = lane >> 4, r = lane & 15;
-  const int blocks = (K + kBlock - 1) / kBlock, kg = K / G;
-  const int n0 = blockIdx.x * 16, t0 = blockIdx.y * 16;
-  const int n = min(n0 + r, N - 1), t = min(t0 + r, T - 1);
-  const uint4* wrow = packed + (int64_t)n * blocks * 4 + q;
-  const int8_t* xrow = xq + (int64_t)t * K + 8 * q;
-  const uint16_t* srow = scales + (int64_t)n * kg;
-  const int8_t* zrow = ZEROS ? zeros + (int64_t)n * kg : nullptr;
+typedef __attribute__((address_space(3))) void* lds_ptr_t;
+typedef __attribute__((address_space(1))) void* glb_ptr_t;
 
-  float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-  for (int b = wave; b < blocks; b += kWaves) {
-    const uint4 p = wrow[b * 4];
-    const uint32_t word[4] = {p.x, p.y, p.z, p.w};
-    uint2 x[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int k = b * kBlock + 32 * j;
-      x[j] = k < K ? *reinterpret_cast<const uint2*>(xrow + k) : make_uint2(0, 0);
-    }
-    auto lo = [&](int j) { return (int)((word[j] << 4) & 0xF0F0F0F0u); };
-    auto hi = [&](int j) { return (int)(word[j] & 0xF0F0F0F0u); };
-    auto scaled = [&](const v4i& acc, const v4i& ones, int g) {
-      const int gi = b * (kBlock / G) + g;
-      if (gi >= kg) return;                           // past K: codes and tokens are 0
-      const float s = bf16_f(srow[gi]);
-      const int z = ZEROS ? 16 * zrow[gi] : 0;
-#pragma unroll
-      for (int v = 0; v < 4; ++v) {
-        const int a = ZEROS ? acc[v] - z * ones[v] : acc[v];
-        sum[v] = fmaf((float)a, s, sum[v]);
-      }
-    };
-    if constexpr (G == 32) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const long a = (long)(((unsigned long)x[j].y << 32) | x[j].x);
-        const long bb = (long)(((unsigned long)(uint32_t)hi(j) << 32) | (uint32_t)lo(j));
-        v4i acc = {0, 0, 0, 0}, one = {0, 0, 0, 0};
-        acc = __builtin_amdgcn_mfma_i32_16x16x32_i8(a, bb, acc, 0, 0, 0);
-        if (ZEROS) one = __builtin_amdgcn_mfma_i32_16x16x32_i8(a, 0x0101010101010101l, one, 0, 0, 0);
-        scaled(acc, one, j);
-      }
+// Eight codes of a packed word, times 16, as two int8 operand words.
+__device__ __forceinline__ int low16(uint32_t w) { return (int)((w << 4) & 0xF0F0F0F0u); }
+__device__ __forceinline__ int high16(uint32_t w) { return (int)(w & 0xF0F0F0F0u); }
+
+// Eight codes less their group's zero point, as two int8 operand words: bytes
+// 0x80 + (t + 8) - (z + 8), none of which borrows from the next, with the sign
+// bit turned over (t - z lies in [-15, 15]).
+__device__ __forceinline__ uint32_t zero_bytes(int z) { return (uint32_t)(z + 8) * 0x01010101u; }
+__device__ __forceinline__ int less_zero(uint32_t c, uint32_t zz) {
+  return (int)(((c | 0x80808080u) - zz) ^ 0x80808080u);
+}
+__device__ __forceinline__ int low_z(uint32_t w, uint32_t zz) {
+  return less_zero((w ^ 0x88888888u) & 0x0F0F0F0Fu, zz);
+}
+__device__ __forceinline__ int high_z(uint32_t w, uint32_t zz) {
+  return less_zero(((w ^ 0x88888888u) >> 4) & 0x0F0F0F0Fu, zz);
+}
+
+// CNT consecutive scales (or zero points) of a row.  Rows have any alignment:
+// inside a row they are loaded in as few pieces as there are words, which the
+// hardware takes at any address; a run that may reach past the row's end
+// (TAIL) goes element by element, those past the end as 0.
+template <typename E, int CNT>
+struct Run {
+  static constexpr int kWords = (CNT * (int)sizeof(E) + 3) / 4;
+  uint32_t w[kWords];
+  template <bool TAIL>
+  __device__ __forceinline__ void load(const E* __restrict__ row, int at, int end) {
+    if constexpr (!TAIL) {
+      __builtin_memcpy(w, row + at, CNT * sizeof(E));
     } else {
-      const v4i one8 = {0x01010101, 0x01010101, 0x01010101, 0x01010101};
-      v4i acc = {0, 0, 0, 0}, one = {0, 0, 0, 0};
+      using U = std::make_unsigned_t<E>;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const v4i a = {(int)x[2 * i].x, (int)x[2 * i].y, (int)x[2 * i + 1].x, (int)x[2 * i + 1].y};
-        const v4i bb = {lo(2 * i), hi(2 * i), lo(2 * i + 1), hi(2 * i + 1)};
-        acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(a, bb, acc, 0, 0, 0);
-        if (ZEROS) one = __builtin_amdgcn_mfma_i32_16x16x64_i8(a, one8, one, 0, 0, 0);
-        if (G == 64 || i == 1) {
-          scaled(acc, one, G == 64 ? i : 0);
-          acc = one = v4i{0, 0, 0, 0};
-        }
+      for (int i = 0; i < kWords; ++i) w[i] = 0;
+#pragma unroll
+      for (int i = 0; i < CNT; ++i) {
+        const uint32_t e = (U)row[min(at + i, end - 1)];
+        constexpr int kPer = 4 / (int)sizeof(E);
+        w[i / kPer] |= (at + i < end ? e : 0u) << (8 * (int)sizeof(E) * (i % kPer));
       }
     }
   }
+  __device__ __forceinline__ float scale(int i) const {    // E = uint16_t
+    return __uint_as_float(i & 1 ? w[i >> 1] & 0xffff0000u : w[i >> 1] << 16);
+  }
+  __device__ __forceinline__ int zero(int i) const {       // E = int8_t
+    return (int)(w[i >> 2] << (24 - 8 * (i & 3))) >> 24;
+  }
+};
+
+// Blocks of 128 k that a wave of k_w4_few loads at a time, into each of two
+// buffers (2560 -> 128256, one token: 2 / 4 / 5 / 8 blocks 34.7 / 34.5 / 35.0
+// / 40.0 us; 8192 -> 28672: 34.6 / 28.9 / 34.4 / 31.4).
+constexpr int kAhead = 4;
+
+// LDS row stride of a token: whole blocks of 128 k, and 16 bytes that spread
+// the rows of one operand read over the banks.
+__host__ __device__ constexpr int token_stride(int k) { return ((k + 127) & ~127) + 16; }
+
+// Up to 16 tokens (decode): the weights stream once.  The tokens' int8 rows are
+// in LDS, permuted so that a lane's 32 bytes of a block of 128 lie together
+// (chunk q of the packed block: k = 32j + 8q + i at byte 32q + 8j + i).  A
+// team of `team` waves has 16 weight rows and splits their blocks into runs; a
+// wave holds two buffers of U blocks (1 KiB each), one on its way while it
+// works on the other, and goes on to its next rows without a pause where it is
+// a team of its own.
+// NV: result registers in use (1: one token, 4: up to 16).
+template <int G, bool ZEROS, int NV, int U>
+__global__ __launch_bounds__(512) void k_w4_few(const uint4* __restrict__ packed,
+                                                const uint16_t* __restrict__ scales,
+                                                const int8_t* __restrict__ zeros,
+                                                const int8_t* __restrict__ xq,
+                                                const float* __restrict__ absmax, int T, int N,
+                                                int K, int team, float* __restrict__ y) {
+  constexpr int NG = kBlock / G;                    // groups per block
+  extern __shared__ __align__(16) unsigned char xs[];   // [T][token_stride(K)]
+  __shared__ float red[8][NV][64];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int q = lane >> 4, r = lane & 15;
+  const int blocks = (K + kBlock - 1) / kBlock, kg = K / G, stride = token_stride(K);
+  const int tiles = (N + 15) / 16, teams = 8 / team;
+  const int part = wave % team;
+  const int per = (blocks + team - 1) / team;       // blocks of a wave's run
+  const int b0 = part * per, b1 = min(b0 + per, blocks);
+  const int runs = (max(b1 - b0, 0) + U - 1) / U;   // its groups of U, per tile
+
+  // tokens: 4 bytes per lane straight into LDS; dword d of a row is word
+  // (d / 2 % 4) of chunk (d / 8 % 4) of its block
+  for (int t = wave; t < T; t += 8) {
+    const int8_t* src = xq + (int64_t)t * K;
+    for (int d0 = 0; d0 < blocks * 32; d0 += 64) {
+      const int d = d0 + lane;
+      const int k = (d >> 5) * kBlock + 32 * ((d >> 1) & 3) + 8 * ((d >> 3) & 3) + 4 * (d & 1);
+      if (d < blocks * 32) {
+        if (k < K)
+          __builtin_amdgcn_global_load_lds((glb_ptr_t)(src + k), (lds_ptr_t)(xs + t * stride + 4 * d0),
+                                           4, 0, 0);
+        else
+          *reinterpret_cast<uint32_t*>(xs + t * stride + 4 * d) = 0;
+      }
+    }
+  }
+  __builtin_amdgcn_sched_barrier(0);
+
+  struct Buf {
+    Run<uint16_t, U * NG> s;
+    Run<int8_t, U * NG> z;
+    uint4 w[U];
+  };
+  // group `g` of the tile's: rows past N read row N - 1, blocks past the run
+  // its last one (their sums are left out)
+  auto load = [&](Buf& b, int tile, int g) {
+    const int n = min(tile * 16 + r, N - 1), c = b0 + g * U;
+    const uint16_t* srow = scales + (int64_t)n * kg;
+    const int8_t* zrow = ZEROS ? zeros + (int64_t)n * kg : nullptr;
+    if ((c + U) * NG <= kg) {
+      b.s.template load<false>(srow, c * NG, kg);
+      if constexpr (ZEROS) b.z.template load<false>(zrow, c * NG, kg);
+    } else {
+      b.s.template load<true>(srow, c * NG, kg);
+      if constexpr (ZEROS) b.z.template load<true>(zrow, c * NG, kg);
+    }
+    const uint4* row = packed + (int64_t)n * blocks * 4 + q;
 #pragma unroll
-  for (int v = 0; v < 4; ++v) red[wave][v][lane] = sum[v];
-  __syncthreads();
-  // lane 16 a + c of register v holds token 4a + v, weight row c
-  const int tok = threadIdx.x >> 4, col = threadIdx.x & 15;
-  if (t0 + tok >= T || n0 + col >= N) return;
-  float s = 0.0f;
+    for (int u = 0; u < U; ++u) b.w[u] = row[4 * min(c + u, blocks - 1)];
+  };
+  float sum[NV];
 #pragma unroll
-  for (int w = 0; w < kWaves; ++w) s += red[w][tok & 3][(tok >> 2) * 16 + col];
-  const float m = fmaxf(absmax[t0 + tok], kEps) / kQb;
-  y[(int64_t)(t0 + tok) * N + n0 + col] = s * (m * 0.0625f);
+  for (int v = 0; v < NV; ++v) sum[v] = 0.0f;
+  const unsigned char* xrow = xs + min(r, T - 1) * stride + 32 * q;
+  auto work = [&](const Buf& b, int g) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int c = b0 + g * U + u;
+      if (c >= b1) break;                           // wave-uniform
+      const uint4* xv = reinterpret_cast<const uint4*>(xrow + c * kBlock);
+      const uint4 xa = xv[0], xb = xv[1];           // words j = 0, 1 and 2, 3
+      const uint32_t w[4] = {b.w[u].x, b.w[u].y, b.w[u].z, b.w[u].w};
+      auto add = [&](const v4i& acc, int i) {
+        const float s = b.s.scale(u * NG + i);
+#pragma unroll
+        for (int v = 0; v < NV; ++v) sum[v] = fmaf((float)acc[v], s, sum[v]);
+      };
+      // operand words of group of 32 number j
+      auto low = [&](int j) {
+        if constexpr (ZEROS) return low_z(w[j], zero_bytes(b.z.zero(u * NG + j * 32 / G)));
+        else return low16(w[j]);
+      };
+      auto high = [&](int j) {
+        if constexpr (ZEROS) return high_z(w[j], zero_bytes(b.z.zero(u * NG + j * 32 / G)));
+        else return high16(w[j]);
+      };
+      const v4i none = {0, 0, 0, 0};
+      if constexpr (G == 32) {
+        const uint2 x[4] = {{xa.x, xa.y}, {xa.z, xa.w}, {xb.x, xb.y}, {xb.z, xb.w}};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const long a = (long)(((unsigned long)x[j].y << 32) | x[j].x);
+          const long w8 = (long)(((unsigned long)(uint32_t)high(j) << 32) | (uint32_t)low(j));
+          add(__builtin_amdgcn_mfma_i32_16x16x32_i8(a, w8, none, 0, 0, 0), j);
+        }
+      } else {
+        const v4i x[2] = {{(int)xa.x, (int)xa.y, (int)xa.z, (int)xa.w},
+                          {(int)xb.x, (int)xb.y, (int)xb.z, (int)xb.w}};
+        v4i acc = none;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(
+              x[i], v4i{low(2 * i), high(2 * i), low(2 * i + 1), high(2 * i + 1)}, acc, 0, 0, 0);
+          if (G == 64 || i == 1) {
+            add(acc, G == 64 ? i : 0);
+            acc = none;
+          }
+        }
+      }
+    }
+  };
+  // lane 16 a + c of register v: token 4a + v, weight row c
+  auto store = [&](int tile) {
+    const int n = tile * 16 + r;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int t = 4 * q + v;
+      if (n < N && t < T && (NV > 1 || q == 0))
+        y[(int64_t)t * N + n] = sum[v] * (fmaxf(absmax[t], kEps) / kQb * (ZEROS ? 1.0f : 0.0625f));
+      sum[v] = 0.0f;
+    }
+  };
+
+  const int step = (int)gridDim.x * teams, first = (int)blockIdx.x * teams + wave / team;
+  Buf buf[2];
+  const bool busy = runs > 0 && first < tiles;
+  if (busy) load(buf[0], first, 0);
+  __builtin_amdgcn_sched_barrier(0);
+  if (busy) wait_vmem<U>();                         // this wave's tokens are in LDS
+  else wait_vmem<0>();
+  lds_sync();
+  if (team == 1) {
+    // one run of groups over all of the wave's tiles, two buffers in turn
+    int tile = first, g = 0, ntile = first, ng = 0;   // group in work; group on its way
+    auto next = [&](Buf& b) {
+      if (++ng == runs) {
+        ng = 0;
+        ntile += step;
+      }
+      if (ntile < tiles) load(b, ntile, ng);
+    };
+    auto turn = [&](Buf& now, Buf& then) {
+      next(then);
+      work(now, g);
+      if (++g == runs) {
+        store(tile);
+        g = 0;
+        tile += step;
+      }
+    };
+    while (tile < tiles) {
+      turn(buf[0], buf[1]);
+      if (tile >= tiles) break;
+      turn(buf[1], buf[0]);
+    }
+  } else {
+    // every team of the block as often, for the barriers
+    for (int base = (int)blockIdx.x * teams; base < tiles; base += step) {
+      const int tile = base + wave / team;
+      if (tile < tiles) {
+        for (int g = 0; g < runs; g += 2) {
+          if (g + 1 < runs) load(buf[1], tile, g + 1);
+          work(buf[0], g);
+          if (g + 2 < runs) load(buf[0], tile, g + 2);
+          if (g + 1 < runs) work(buf[1], g + 1);
+        }
+#pragma unroll
+        for (int v = 0; v < NV; ++v) red[wave][v][lane] = sum[v];
+      }
+      if (runs > 0 && tile + step < tiles) load(buf[0], tile + step, 0);
+      lds_sync();
+      if (part == 0 && tile < tiles) {
+#pragma unroll
+        for (int v = 0; v < NV; ++v)
+          for (int w = 1; w < team; ++w) sum[v] += red[wave + w][v][lane];
+        store(tile);
+      }
+#pragma unroll
+      for (int v = 0; v < NV; ++v) sum[v] = 0.0f;
+      if (base + step < tiles) lds_sync();          // red is free again
+    }
+  }
+}
+
+// Many tokens: int8 tokens through LDS (global -> LDS directly, three stages,
+// one barrier per 128 k), weights straight into registers, WMF row fragments
+// of 32 x 32 per wave on v_mfma_i32_32x32x32_i8.  Lane (m, h) takes chunks 2h
+// and 2h + 1 of weight row m: word j of the two is 16 consecutive k of the
+// block's group of 32 number j.
+//
+// A group's sums are converted and scaled in registers, two VALU operations of
+// four cycles per register and group, against 32 cycles of MFMA per 32 k and
+// fragment: for groups of 32 and 64 that, not the matrix cores, bounds the
+// kernel.  So the products of one fragment and group are issued ahead of the
+// scaling of the one before.  Zero points come off the codes (t - z fits
+// an int8; five more operations per word, which all row fragments share) and
+// not off the sums (two operations per register).
+//
+// WK > 1 (few tiles): WK groups of waves split K, each with its own stages,
+// and add their sums through LDS in order.
+template <int WN, int WK, int WMF, int G, bool ZEROS, bool TAIL>
+__global__ __launch_bounds__(WN * WK * 64, WMF == 2 ? 3 : 1) void k_w4_tile(const uint4* __restrict__ packed,
+                                                          const uint16_t* __restrict__ scales,
+                                                          const int8_t* __restrict__ zeros,
+                                                          const int8_t* __restrict__ xq,
+                                                          const float* __restrict__ absmax, int T,
+                                                          int N, int K, float* __restrict__ y) {
+  constexpr int NG = kBlock / G;
+  constexpr int BM = 32 * WMF, BN = 32 * WN, kThreads = WN * WK * 64;
+  constexpr int kATot = BM / 8, kAChunks = (kATot + WN - 1) / WN;   // 1 KiB pieces of a stage
+  constexpr int kStage = BM * kBlock;
+  __shared__ __align__(16) unsigned char A0[WK * kStage], A1[WK * kStage], A2[WK * kStage];
+  __shared__ float scale[BM];
+  __shared__ float red[WK > 1 ? (WK - 1) * WN : 1][WK > 1 ? WMF * 16 : 1][64];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wn = wave % WN, wk = wave / WN;
+  auto stage_of = [&](auto st) -> unsigned char* {
+    constexpr int S = decltype(st)::value;
+    if constexpr (S == 0) return A0 + wk * kStage;
+    else if constexpr (S == 1) return A1 + wk * kStage;
+    else return A2 + wk * kStage;
+  };
+  const int h = lane >> 5, m = lane & 31;
+  const int blocks = (K + kBlock - 1) / kBlock, kg = K / G;
+  const int per = (blocks + WK - 1) / WK;           // blocks of 128 k per group of waves
+  const int b0 = min(wk * per, blocks - 1), nb = min(per, blocks - wk * per);   // nb < 1: none
+
+  // tiles in equal runs to the XCDs, four row blocks at a time, down the rows first
+  const int64_t ntn = (N + BN - 1) / BN, ntm = (T + BM - 1) / BM, tiles = ntn * ntm;
+  const int64_t per_xcd = (tiles + 7) / 8;
+  const int64_t tile = (blockIdx.x % 8) * per_xcd + blockIdx.x / 8;
+  if (blockIdx.x / 8 >= per_xcd || tile >= tiles) return;
+  const int64_t gid = tile / (4 * ntn), first_m = gid * 4, r_in = tile - gid * 4 * ntn;
+  const int64_t gsize = ntm - first_m < 4 ? ntm - first_m : 4;
+  const int m0 = (int)(first_m + r_in % gsize) * BM, n0 = (int)(r_in / gsize) * BN;
+
+  // without zero points the codes are 16 t
+  for (int i = tid; i < BM; i += kThreads)
+    scale[i] = m0 + i < T ? fmaxf(absmax[m0 + i], kEps) / kQb * (ZEROS ? 1.0f : 0.0625f) : 0.0f;
+
+  // activations: 1 KiB = 8 rows x 128 bytes; row r's 16-byte slot p holds slot
+  // p ^ ((r >> 1) & 7), which spreads an operand read over the banks.  Slots
+  // past K meet codes of 0 and scales of 0: they take the row's last bytes
+  const int8_t* asrc[kAChunks];
+  int aslot[kAChunks];
+#pragma unroll
+  for (int i = 0; i < kAChunks; ++i) {
+    const int c = min(wn * kAChunks + i, kATot - 1), row = 8 * c + (lane >> 3);
+    asrc[i] = xq + (int64_t)min(m0 + row, T - 1) * K;
+    aslot[i] = 16 * ((lane & 7) ^ ((row >> 1) & 7));
+  }
+  const int64_t n = min(n0 + wn * 32 + m, N - 1);
+  const uint4* wsrc = packed + n * blocks * 4 + 2 * h;
+  const uint16_t* ssrc = scales + n * kg;
+  const int8_t* zsrc = ZEROS ? zeros + n * kg : nullptr;
+  struct Frag {
+    uint4 w0, w1;
+    Run<uint16_t, NG> s;
+    Run<int8_t, NG> z;
+  };
+  Frag frag[3];
+  auto issue = [&](int i, auto st) {                // block i of this group's, the last one again past it
+    constexpr int S = decltype(st)::value;
+    const int b = b0 + max(min(i, nb - 1), 0);
+#pragma unroll
+    for (int u = 0; u < kAChunks; ++u)
+      __builtin_amdgcn_global_load_lds(
+          (glb_ptr_t)(asrc[u] + min(b * kBlock + aslot[u], K - 16)),
+          (lds_ptr_t)(stage_of(st) + min(wn * kAChunks + u, kATot - 1) * 1024), 16, 0, 0);
+    frag[S].s.template load<TAIL>(ssrc, b * NG, kg);
+    if constexpr (ZEROS) frag[S].z.template load<TAIL>(zsrc, b * NG, kg);
+    frag[S].w0 = wsrc[4 * b];
+    frag[S].w1 = wsrc[4 * b + 1];
+  };
+  constexpr int kLoads = kAChunks + 3 + ZEROS;      // at least: a wave's loads per step
+
+  v16f sum[WMF];
+#pragma unroll
+  for (int i = 0; i < WMF; ++i)
+#pragma unroll
+    for (int v = 0; v < 16; ++v) sum[i][v] = 0.0f;
+
+  using I0 = std::integral_constant<int, 0>;
+  using I1 = std::integral_constant<int, 1>;
+  using I2 = std::integral_constant<int, 2>;
+  __builtin_amdgcn_s_waitcnt(0);
+  issue(0, I0{});
+  issue(1, I1{});
+  wait_vmem<kLoads>();
+  lds_sync();
+
+  const int swz = (m >> 1) & 7;
+  auto step = [&](auto st, int b) {
+    constexpr int S = decltype(st)::value;
+    using R = std::integral_constant<int, (S + 2) % 3>;
+    issue(b + 2, R{});
+    const unsigned char* At = stage_of(st) + m * kBlock;
+    if (WK == 1 || b < nb) {
+      // operand words of the block's four groups of 32
+      v4i w[4];
+      const uint32_t u[8] = {frag[S].w0.x, frag[S].w0.y, frag[S].w0.z, frag[S].w0.w,
+                             frag[S].w1.x, frag[S].w1.y, frag[S].w1.z, frag[S].w1.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if constexpr (!ZEROS) {
+          w[j] = v4i{low16(u[j]), high16(u[j]), low16(u[4 + j]), high16(u[4 + j])};
+        } else {
+          const uint32_t zz = zero_bytes(frag[S].z.zero(j / (G / 32)));
+          w[j] = v4i{low_z(u[j], zz), high_z(u[j], zz), low_z(u[4 + j], zz), high_z(u[4 + j], zz)};
+        }
+      }
+      v16i zero;
+#pragma unroll
+      for (int v = 0; v < 16; ++v) zero[v] = 0;
+#pragma unroll
+      for (int g = 0; g < NG; ++g) {
+        v16i acc[WMF];
+#pragma unroll
+        for (int jj = 0; jj < G / 32; ++jj) {
+          const int j = g * (G / 32) + jj;
+#pragma unroll
+          for (int i = 0; i < WMF; ++i) {
+            const uint4 t = *reinterpret_cast<const uint4*>(At + i * 32 * kBlock + 16 * ((2 * j + h) ^ swz));
+            acc[i] = __builtin_amdgcn_mfma_i32_32x32x32_i8(
+                v4i{(int)t.x, (int)t.y, (int)t.z, (int)t.w}, w[j], jj ? acc[i] : zero, 0, 0, 0);
+          }
+        }
+        const float s = frag[S].s.scale(g);
+#pragma unroll
+        for (int i = 0; i < WMF; ++i)
+#pragma unroll
+          for (int v = 0; v < 16; ++v) sum[i][v] = fmaf((float)acc[i][v], s, sum[i][v]);
+      }
+    }
+    wait_vmem<kLoads>();
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  int b = 0;
+  for (; b + 3 <= per; b += 3) {
+    step(I0{}, b);
+    step(I1{}, b + 1);
+    step(I2{}, b + 2);
+  }
+  if (b < per) step(I0{}, b);
+  if (b + 1 < per) step(I1{}, b + 1);
+  wait_vmem<0>();   // no load may land in LDS after the block has finished
+
+  if constexpr (WK > 1) {
+    if (wk > 0) {
+#pragma unroll
+      for (int i = 0; i < WMF; ++i)
+#pragma unroll
+        for (int v = 0; v < 16; ++v) red[wave - WN][i * 16 + v][lane] = sum[i][v];
+    }
+    lds_sync();
+    if (wk > 0) return;
+#pragma unroll
+    for (int i = 0; i < WMF; ++i)
+#pragma unroll
+      for (int v = 0; v < 16; ++v)
+        for (int k = 0; k < WK - 1; ++k) sum[i][v] += red[k * WN + wn][i * 16 + v][lane];
+  }
+  const int col = n0 + wn * 32 + m;
+#pragma unroll
+  for (int i = 0; i < WMF; ++i)
+#pragma unroll
+    for (int v = 0; v < 16; ++v) {
+      const int row = i * 32 + (v >> 2) * 8 + h * 4 + (v & 3);
+      if (m0 + row < T && col < N) y[(int64_t)(m0 + row) * N + col] = sum[i][v] * scale[row];
+    }
 }
 
 unsigned stream_grid(int64_t units) {
@@ -260,14 +622,68 @@ hipError_t launch_unpack_w4(const uint8_t* packed, const uint16_t* scales, const
 hipError_t launch_forward_w4(const uint8_t* packed, const uint16_t* scales, const int8_t* zeros,
                              const int8_t* xq, const float* absmax, int64_t t, int64_t n,
                              int64_t k, int g, float* y, hipStream_t stream) {
-  // grid.y holds at most 65535 blocks: more tokens go in several launches
-  for (int64_t t0 = 0; t0 < t; t0 += 65535 * 16) {
-    const int64_t nt = std::min<int64_t>(t - t0, 65535 * 16);
-    const dim3 grid((unsigned)((n + 15) / 16), (unsigned)((nt + 15) / 16));
-    const hipError_t e = by_group(g, zeros != nullptr, [&](auto gc, auto zc) {
-      k_w4_rows<decltype(gc)::value, decltype(zc)::value><<<grid, 256, 0, stream>>>(
-          reinterpret_cast<const uint4*>(packed), scales, zeros, xq + t0 * k, absmax + t0, (int)nt,
-          (int)n, (int)k, y + t0 * n);
+  const auto* w = reinterpret_cast<const uint4*>(packed);
+  if (t > 16) {
+    const int64_t cus = device_cus();
+    auto tiles = [&](int64_t rows, int64_t cols) {
+      return ((t + rows - 1) / rows) * ((n + cols - 1) / cols);
+    };
+    return by_group(g, zeros != nullptr, [&](auto gc, auto zc) {
+      constexpr int G = decltype(gc)::value;
+      constexpr bool Z = decltype(zc)::value;
+      auto go = [&](auto wn, auto wk, auto wmf) {
+        constexpr int WN = decltype(wn)::value, WK = decltype(wk)::value, WMF = decltype(wmf)::value;
+        auto kern = k_w4_tile<WN, WK, WMF, G, Z, false>;
+        if constexpr (G < kBlock)
+          if (k % kBlock) kern = k_w4_tile<WN, WK, WMF, G, Z, true>;
+        kern<<<(unsigned)((tiles(32 * WMF, 32 * WN) + 7) / 8 * 8), 64 * WN * WK, 0, stream>>>(
+            w, scales, zeros, xq, absmax, (int)t, (int)n, (int)k, y);
+      };
+      using I1 = std::integral_constant<int, 1>;
+      using I2 = std::integral_constant<int, 2>;
+      using I4 = std::integral_constant<int, 4>;
+      using I8 = std::integral_constant<int, 8>;
+      // the smallest tiles, with K split most, that do not outnumber the CUs
+      // (see above)
+      if (tiles(32, 32) <= cus) return go(I1{}, I8{}, I1{});
+      if (tiles(32, 64) <= cus) return go(I2{}, I4{}, I1{});
+      if (tiles(32, 128) <= cus) return go(I4{}, I2{}, I1{});
+      if (G == 128 && 8 * tiles(128, 256) >= 5 * cus) return go(I8{}, I1{}, I4{});
+      if (4 * tiles(64, 128) >= 5 * cus) return go(I4{}, I1{}, I2{});
+      return go(I4{}, I1{}, I1{});
+    });
+  }
+  // as many tokens at a time as LDS holds
+  const int64_t stride = token_stride((int)k), most = std::min<int64_t>(16, kMaxLds / stride);
+  const int64_t tiles = (n + 15) / 16, blocks = (k + kBlock - 1) / kBlock;
+  // K split over a team of waves while there are too few tiles to fill the
+  // device and a wave would have more than one load group (2560 -> 2560, one
+  // token: teams of 4 / 8 5.2 / 4.3 us; 2560 -> 16384: 1 / 2 / 4 8.2 / 8.6 / 8.5).
+  // Several tokens are staged by every block, so for them fewer, larger ones
+  // (2560 -> 6912, 7 tokens, groups of 32: teams of 4 / 8 10.1 / 13.5 us).
+  const int64_t want = t == 1 ? 2048 : 1024;
+  int team = 1;
+  while (team < 8 && tiles * team < want && blocks > kAhead * team) team *= 2;
+  for (int64_t t0 = 0; t0 < t; t0 += most) {
+    const int64_t nt = std::min(t - t0, most);
+    const size_t lds = (size_t)(nt * stride);
+    // two blocks per CU where their LDS fits, going on from tile to tile
+    // (2560 -> 128256, one token: 1 / 2 / 3 / 4 blocks 43 / 33 / 35 / 34 us)
+    const int64_t per_cu = lds + 12288 <= (size_t)kMaxLds / 2 ? 2 : 1;
+    const int64_t grid = std::min<int64_t>((tiles * team + 7) / 8, per_cu * device_cus());
+    hipError_t e = hipSuccess;
+    by_group(g, zeros != nullptr, [&](auto gc, auto zc) {
+      constexpr int G = decltype(gc)::value;
+      constexpr bool Z = decltype(zc)::value;
+      auto go = [&](auto kern) {
+        e = kern.allow_lds();
+        if (e != hipSuccess) return;
+        kern.kernel<<<(unsigned)grid, 512, lds, stream>>>(w, scales, zeros, xq + t0 * k, absmax + t0,
+                                                   (int)nt, (int)n, (int)k, team, y + t0 * n);
+        e = hipGetLastError();
+      };
+      if (nt == 1) go(Kernel<k_w4_few<G, Z, 1, kAhead>>{});
+      else go(Kernel<k_w4_few<G, Z, 4, kAhead>>{});
     });
     if (e != hipSuccess) return e;
   }
