@@ -35,18 +35,18 @@ __device__ __forceinline__ uint16_t f_bf16(float f) {   // finite f >= 0, neares
 // Four neighbouring lanes hold one block of a row: lane q its 16-byte chunk,
 // weights k = 32j + 8q + i.  A group of 32, 64 or 128 is one, two or four of
 // the j over the four lanes.
-template <int G, bool ZEROS>
-__global__ __launch_bounds__(256) void k_pack_w4(const float* __restrict__ w, int64_t n, int K,
+template <int G, bool ZEROS, typename INDEX>
+__global__ __launch_bounds__(256) void k_pack_w4(const float* __restrict__ w, INDEX units, int K,
                                                  uint4* __restrict__ packed,
                                                  uint16_t* __restrict__ scales,
                                                  int8_t* __restrict__ zeros) {
   constexpr int GJ = G / 32, NG = 4 / GJ;           // words per group, groups per block
-  const int blocks = (K + kBlock - 1) / kBlock, kg = K / G;
-  const int64_t units = n * blocks * 4;
-  const int64_t step = (int64_t)gridDim.x * 256;
-  for (int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x; u < units; u += step) {
-    const int64_t b = u >> 2, row = b / blocks;
-    const int q = (int)(u & 3), blk = (int)(b - row * blocks);
+  const INDEX blocks = (INDEX)((K + kBlock - 1) / kBlock);
+  const int kg = K / G;
+  for (INDEX u = (INDEX)blockIdx.x * 256 + threadIdx.x; u < units; u += (INDEX)gridDim.x * 256) {
+    const INDEX b = u >> 2;
+    const int64_t row = b / blocks;
+    const int q = (int)(u & 3), blk = (int)(b - (INDEX)row * blocks);
     float v[4][8];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -102,36 +102,32 @@ __global__ __launch_bounds__(256) void k_pack_w4(const float* __restrict__ w, in
   }
 }
 
-template <bool ZEROS>
+// Eight neighbouring lanes hold one block of a row, lane (q, p) the low (p = 0)
+// or high nibbles of chunk q: per word j they write 128 consecutive bytes.
+// INDEX: a 32-bit unsigned type where it numbers all lanes.
+template <bool ZEROS, typename INDEX>
 __global__ __launch_bounds__(256) void k_unpack_w4(const uint4* __restrict__ packed,
                                                    const uint16_t* __restrict__ scales,
-                                                   const int8_t* __restrict__ zeros, int64_t n,
+                                                   const int8_t* __restrict__ zeros, INDEX units,
                                                    int K, int G, float* __restrict__ w) {
-  const int blocks = (K + kBlock - 1) / kBlock, kg = K / G;
-  const int64_t units = n * blocks * 4;
-  const int64_t step = (int64_t)gridDim.x * 256;
-  for (int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x; u < units; u += step) {
-    const int64_t b = u >> 2, row = b / blocks;
-    const int q = (int)(u & 3), blk = (int)(b - row * blocks);
-    const uint4 p = packed[u];
-    const uint32_t word[4] = {p.x, p.y, p.z, p.w};
+  const INDEX blocks = (INDEX)((K + kBlock - 1) / kBlock);
+  const int kg = K / G;
+  for (INDEX u = (INDEX)blockIdx.x * 256 + threadIdx.x; u < units; u += (INDEX)gridDim.x * 256) {
+    const INDEX b = u >> 3, row = b / blocks;
+    const int p = (int)(u & 1), q = (int)(u >> 1 & 3), blk = (int)(b - row * blocks);
+    const uint4 v = packed[(int64_t)(u >> 1)];
+    const uint32_t word[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const int k = blk * kBlock + 32 * j + 8 * q;
+      const int k = blk * kBlock + 32 * j + 8 * q + 4 * p;
       if (k >= K) continue;
-      const int64_t gi = row * kg + k / G;
+      const int64_t gi = (int64_t)row * kg + k / G;
       const float s = bf16_f(scales[gi]);
       const int z = ZEROS ? zeros[gi] : 0;
-      float f[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int sh = 8 * (i & 3) + 4 * (i >> 2);
-        const int t = (int)(word[j] << (28 - sh)) >> 28;
-        f[i] = (float)(t - z) * s;
-      }
-      float4* dst = reinterpret_cast<float4*>(w + row * K + k);
-      dst[0] = make_float4(f[0], f[1], f[2], f[3]);
-      dst[1] = make_float4(f[4], f[5], f[6], f[7]);
+      const uint32_t c = p ? word[j] : word[j] << 4;
+      auto value = [&](int i) { return (float)(((int)(c << (24 - 8 * i)) >> 28) - z) * s; };
+      *reinterpret_cast<float4*>(w + (int64_t)row * K + k) =
+          make_float4(value(0), value(1), value(2), value(3));
     }
   }
 }
@@ -603,19 +599,32 @@ hipError_t by_group(int g, bool zeros, F&& f) {
 
 hipError_t launch_pack_w4(const float* w, int64_t n, int64_t k, int g, uint8_t* packed,
                           uint16_t* scales, int8_t* zeros, hipStream_t stream) {
-  const unsigned grid = stream_grid(n * ((k + kBlock - 1) / kBlock) * 4);
+  const int64_t units = n * ((k + kBlock - 1) / kBlock) * 4;
+  const unsigned grid = stream_grid(units);
+  const bool small = units + 256 * (int64_t)grid < (int64_t(1) << 32);   // u never wraps
   return by_group(g, zeros != nullptr, [&](auto gc, auto zc) {
-    k_pack_w4<decltype(gc)::value, decltype(zc)::value><<<grid, 256, 0, stream>>>(
-        w, n, (int)k, reinterpret_cast<uint4*>(packed), scales, zeros);
+    auto go = [&](auto ic) {
+      using I = decltype(ic);
+      k_pack_w4<decltype(gc)::value, decltype(zc)::value, I><<<grid, 256, 0, stream>>>(
+          w, (I)units, (int)k, reinterpret_cast<uint4*>(packed), scales, zeros);
+    };
+    small ? go(uint32_t{}) : go(uint64_t{});
   });
 }
 
 hipError_t launch_unpack_w4(const uint8_t* packed, const uint16_t* scales, const int8_t* zeros,
                             int64_t n, int64_t k, int g, float* w, hipStream_t stream) {
-  const unsigned grid = stream_grid(n * ((k + kBlock - 1) / kBlock) * 4);
+  const int64_t units = n * ((k + kBlock - 1) / kBlock) * 8;
+  const unsigned grid = stream_grid(units);
   const auto* p = reinterpret_cast<const uint4*>(packed);
-  if (zeros) k_unpack_w4<true><<<grid, 256, 0, stream>>>(p, scales, zeros, n, (int)k, g, w);
-  else k_unpack_w4<false><<<grid, 256, 0, stream>>>(p, scales, zeros, n, (int)k, g, w);
+  auto go = [&](auto zc, auto ic) {
+    using I = decltype(ic);
+    k_unpack_w4<decltype(zc)::value, I><<<grid, 256, 0, stream>>>(p, scales, zeros, (I)units, (int)k,
+                                                                  g, w);
+  };
+  const bool small = units + 256 * (int64_t)grid < (int64_t(1) << 32);   // u never wraps
+  if (zeros) small ? go(std::true_type{}, uint32_t{}) : go(std::true_type{}, uint64_t{});
+  else small ? go(std::false_type{}, uint32_t{}) : go(std::false_type{}, uint64_t{});
   return hipGetLastError();
 }
 
