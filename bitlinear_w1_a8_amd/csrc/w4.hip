@@ -141,19 +141,13 @@ typedef __attribute__((address_space(1))) void* glb_ptr_t;
 __device__ __forceinline__ int low16(uint32_t w) { return (int)((w << 4) & 0xF0F0F0F0u); }
 __device__ __forceinline__ int high16(uint32_t w) { return (int)(w & 0xF0F0F0F0u); }
 
-// Eight codes less their group's zero point, as two int8 operand words: bytes
-// 0x80 + (t + 8) - (z + 8), none of which borrows from the next, with the sign
-// bit turned over (t - z lies in [-15, 15]).
-__device__ __forceinline__ uint32_t zero_bytes(int z) { return (uint32_t)(z + 8) * 0x01010101u; }
-__device__ __forceinline__ int less_zero(uint32_t c, uint32_t zz) {
-  return (int)(((c | 0x80808080u) - zz) ^ 0x80808080u);
-}
+// Eight codes less their group's zero point, as two int8 operand words: with
+// zz = z + 8 in every byte, bytes 0x80 + (t + 8) - (z + 8), none of which
+// borrows from the next, then the sign bit turned over (t - z lies in [-15, 15]).
 __device__ __forceinline__ int low_z(uint32_t w, uint32_t zz) {
-  return less_zero((w ^ 0x88888888u) & 0x0F0F0F0Fu, zz);
+  return (int)((((w & 0x0F0F0F0Fu) ^ 0x88888888u) - zz) ^ 0x80808080u);
 }
-__device__ __forceinline__ int high_z(uint32_t w, uint32_t zz) {
-  return less_zero(((w ^ 0x88888888u) >> 4) & 0x0F0F0F0Fu, zz);
-}
+__device__ __forceinline__ int high_z(uint32_t w, uint32_t zz) { return low_z(w >> 4, zz); }
 
 // CNT consecutive scales (or zero points) of a row.  Rows have any alignment:
 // inside a row they are loaded in as few pieces as there are words, which the
@@ -182,8 +176,9 @@ struct Run {
   __device__ __forceinline__ float scale(int i) const {    // E = uint16_t
     return __uint_as_float(i & 1 ? w[i >> 1] & 0xffff0000u : w[i >> 1] << 16);
   }
-  __device__ __forceinline__ int zero(int i) const {       // E = int8_t
-    return (int)(w[i >> 2] << (24 - 8 * (i & 3))) >> 24;
+  __device__ __forceinline__ uint32_t zero_bytes(int i) const {   // E = int8_t: z + 8, four times
+    const uint32_t z = __builtin_amdgcn_perm(w[i >> 2], w[i >> 2], 0x01010101u * (uint32_t)(i & 3));
+    return (z ^ 0x08080808u) & 0x0F0F0F0Fu;
   }
 };
 
@@ -197,12 +192,10 @@ constexpr int kAhead = 4;
 __host__ __device__ constexpr int token_stride(int k) { return ((k + 127) & ~127) + 16; }
 
 // Up to 16 tokens (decode): the weights stream once.  The tokens' int8 rows are
-// in LDS, permuted so that a lane's 32 bytes of a block of 128 lie together
-// (chunk q of the packed block: k = 32j + 8q + i at byte 32q + 8j + i).  A
-// team of `team` waves has 16 weight rows and splits their blocks into runs; a
-// wave holds two buffers of U blocks (1 KiB each), one on its way while it
-// works on the other, and goes on to its next rows without a pause where it is
-// a team of its own.
+// whole in LDS.  A team of `team` waves has 16 weight rows and splits their
+// blocks into runs; a wave holds two buffers of U blocks (1 KiB each), one on
+// its way while it works on the other, and goes on to its next rows without a
+// pause where it is a team of its own.
 // NV: result registers in use (1: one token, 4: up to 16).
 template <int G, bool ZEROS, int NV, int U>
 __global__ __launch_bounds__(512) void k_w4_few(const uint4* __restrict__ packed,
@@ -224,20 +217,16 @@ __global__ __launch_bounds__(512) void k_w4_few(const uint4* __restrict__ packed
   const int b0 = part * per, b1 = min(b0 + per, blocks);
   const int runs = (max(b1 - b0, 0) + U - 1) / U;   // its groups of U, per tile
 
-  // tokens: 4 bytes per lane straight into LDS; dword d of a row is word
-  // (d / 2 % 4) of chunk (d / 8 % 4) of its block
+  // tokens: straight into LDS, 16 bytes per lane, zeros past K
   for (int t = wave; t < T; t += 8) {
     const int8_t* src = xq + (int64_t)t * K;
-    for (int d0 = 0; d0 < blocks * 32; d0 += 64) {
-      const int d = d0 + lane;
-      const int k = (d >> 5) * kBlock + 32 * ((d >> 1) & 3) + 8 * ((d >> 3) & 3) + 4 * (d & 1);
-      if (d < blocks * 32) {
-        if (k < K)
-          __builtin_amdgcn_global_load_lds((glb_ptr_t)(src + k), (lds_ptr_t)(xs + t * stride + 4 * d0),
-                                           4, 0, 0);
-        else
-          *reinterpret_cast<uint32_t*>(xs + t * stride + 4 * d) = 0;
-      }
+    for (int k0 = 0; k0 < blocks * kBlock; k0 += 1024) {
+      const int k = k0 + 16 * lane;
+      if (k < K)
+        __builtin_amdgcn_global_load_lds((glb_ptr_t)(src + k), (lds_ptr_t)(xs + t * stride + k0), 16,
+                                         0, 0);
+      else if (k < blocks * kBlock)
+        *reinterpret_cast<uint4*>(xs + t * stride + k) = make_uint4(0, 0, 0, 0);
     }
   }
   __builtin_amdgcn_sched_barrier(0);
@@ -247,10 +236,12 @@ __global__ __launch_bounds__(512) void k_w4_few(const uint4* __restrict__ packed
     Run<int8_t, U * NG> z;
     uint4 w[U];
   };
-  // group `g` of the tile's: rows past N read row N - 1, blocks past the run
-  // its last one (their sums are left out)
+  // First block that group `g` of the run loads: its own, or for the row's last
+  // blocks U before the end, so that a load group lies inside the row.
+  auto first_of = [&](int g) { return max(min(b0 + g * U, blocks - U), 0); };
+  // group `g` of the tile's: rows past N read row N - 1
   auto load = [&](Buf& b, int tile, int g) {
-    const int n = min(tile * 16 + r, N - 1), c = b0 + g * U;
+    const int n = min(tile * 16 + r, N - 1), c = first_of(g);
     const uint16_t* srow = scales + (int64_t)n * kg;
     const int8_t* zrow = ZEROS ? zeros + (int64_t)n * kg : nullptr;
     if ((c + U) * NG <= kg) {
@@ -267,14 +258,16 @@ __global__ __launch_bounds__(512) void k_w4_few(const uint4* __restrict__ packed
   float sum[NV];
 #pragma unroll
   for (int v = 0; v < NV; ++v) sum[v] = 0.0f;
-  const unsigned char* xrow = xs + min(r, T - 1) * stride + 32 * q;
+  const unsigned char* xrow = xs + min(r, T - 1) * stride + 8 * q;
   auto work = [&](const Buf& b, int g) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int c = b0 + g * U + u;
-      if (c >= b1) break;                           // wave-uniform
-      const uint4* xv = reinterpret_cast<const uint4*>(xrow + c * kBlock);
-      const uint4 xa = xv[0], xb = xv[1];           // words j = 0, 1 and 2, 3
+      const int c = first_of(g) + u, lo = b0 + g * U;
+      if ((uint32_t)(c - lo) >= (uint32_t)(b1 - lo)) continue;   // another group's (wave-uniform)
+      uint2 x[4];                                   // the lane's 8 k of each group of 32
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        x[j] = *reinterpret_cast<const uint2*>(xrow + c * kBlock + 32 * j);
       const uint32_t w[4] = {b.w[u].x, b.w[u].y, b.w[u].z, b.w[u].w};
       auto add = [&](const v4i& acc, int i) {
         const float s = b.s.scale(u * NG + i);
@@ -283,16 +276,15 @@ __global__ __launch_bounds__(512) void k_w4_few(const uint4* __restrict__ packed
       };
       // operand words of group of 32 number j
       auto low = [&](int j) {
-        if constexpr (ZEROS) return low_z(w[j], zero_bytes(b.z.zero(u * NG + j * 32 / G)));
+        if constexpr (ZEROS) return low_z(w[j], b.z.zero_bytes(u * NG + j * 32 / G));
         else return low16(w[j]);
       };
       auto high = [&](int j) {
-        if constexpr (ZEROS) return high_z(w[j], zero_bytes(b.z.zero(u * NG + j * 32 / G)));
+        if constexpr (ZEROS) return high_z(w[j], b.z.zero_bytes(u * NG + j * 32 / G));
         else return high16(w[j]);
       };
       const v4i none = {0, 0, 0, 0};
       if constexpr (G == 32) {
-        const uint2 x[4] = {{xa.x, xa.y}, {xa.z, xa.w}, {xb.x, xb.y}, {xb.z, xb.w}};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const long a = (long)(((unsigned long)x[j].y << 32) | x[j].x);
@@ -300,13 +292,12 @@ __global__ __launch_bounds__(512) void k_w4_few(const uint4* __restrict__ packed
           add(__builtin_amdgcn_mfma_i32_16x16x32_i8(a, w8, none, 0, 0, 0), j);
         }
       } else {
-        const v4i x[2] = {{(int)xa.x, (int)xa.y, (int)xa.z, (int)xa.w},
-                          {(int)xb.x, (int)xb.y, (int)xb.z, (int)xb.w}};
         v4i acc = none;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(
-              x[i], v4i{low(2 * i), high(2 * i), low(2 * i + 1), high(2 * i + 1)}, acc, 0, 0, 0);
+              v4i{(int)x[2 * i].x, (int)x[2 * i].y, (int)x[2 * i + 1].x, (int)x[2 * i + 1].y},
+              v4i{low(2 * i), high(2 * i), low(2 * i + 1), high(2 * i + 1)}, acc, 0, 0, 0);
           if (G == 64 || i == 1) {
             add(acc, G == 64 ? i : 0);
             acc = none;
@@ -512,7 +503,7 @@ __global__ __launch_bounds__(WN * WK * 64, WMF == 2 ? 3 : 1) void k_w4_tile(cons
         if constexpr (!ZEROS) {
           w[j] = v4i{low16(u[j]), high16(u[j]), low16(u[4 + j]), high16(u[4 + j])};
         } else {
-          const uint32_t zz = zero_bytes(frag[S].z.zero(j / (G / 32)));
+          const uint32_t zz = frag[S].z.zero_bytes(j / (G / 32));
           w[j] = v4i{low_z(u[j], zz), high_z(u[j], zz), low_z(u[4 + j], zz), high_z(u[4 + j], zz)};
         }
       }
