@@ -483,67 +483,77 @@ __global__ __launch_bounds__(WN * WK * 64, WMF == 2 ? 3 : 1) void k_w4_tile(cons
   using I2 = std::integral_constant<int, 2>;
   __builtin_amdgcn_s_waitcnt(0);
   issue(0, I0{});
+  __builtin_amdgcn_sched_barrier(0);
   issue(1, I1{});
-  wait_vmem<kLoads>();
+  __builtin_amdgcn_sched_barrier(0);
+  wait_vmem<kLoads>();                              // block 0 (the second one stays in flight)
   lds_sync();
 
   const int swz = (m >> 1) & 7;
-  auto step = [&](auto st, int b) {
+  // One block of 128 k on stage S.  REFILL: stage S + 2 takes block b + 2, and
+  // the step ends when all but the loads of that refill have come back; the
+  // last steps load nothing more and wait for all there is.  (With no branch
+  // in the loop and the refill fenced off, a counted wait leaves exactly the
+  // refill in flight.)
+  auto step = [&](auto st, int b, auto refill) {
     constexpr int S = decltype(st)::value;
-    using R = std::integral_constant<int, (S + 2) % 3>;
-    issue(b + 2, R{});
+    constexpr bool REFILL = decltype(refill)::value;
+    if constexpr (REFILL) {
+      issue(b + 2, std::integral_constant<int, (S + 2) % 3>{});
+      __builtin_amdgcn_sched_barrier(0);
+    }
     const unsigned char* At = stage_of(st) + m * kBlock;
-    if (WK == 1 || b < nb) {
-      // operand words of the block's four groups of 32
-      v4i w[4];
-      const uint32_t u[8] = {frag[S].w0.x, frag[S].w0.y, frag[S].w0.z, frag[S].w0.w,
-                             frag[S].w1.x, frag[S].w1.y, frag[S].w1.z, frag[S].w1.w};
+    // operand words of the block's four groups of 32
+    v4i w[4];
+    const uint32_t u[8] = {frag[S].w0.x, frag[S].w0.y, frag[S].w0.z, frag[S].w0.w,
+                           frag[S].w1.x, frag[S].w1.y, frag[S].w1.z, frag[S].w1.w};
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if constexpr (!ZEROS) {
-          w[j] = v4i{low16(u[j]), high16(u[j]), low16(u[4 + j]), high16(u[4 + j])};
-        } else {
-          const uint32_t zz = frag[S].z.zero_bytes(j / (G / 32));
-          w[j] = v4i{low_z(u[j], zz), high_z(u[j], zz), low_z(u[4 + j], zz), high_z(u[4 + j], zz)};
-        }
-      }
-      v16i zero;
-#pragma unroll
-      for (int v = 0; v < 16; ++v) zero[v] = 0;
-#pragma unroll
-      for (int g = 0; g < NG; ++g) {
-        v16i acc[WMF];
-#pragma unroll
-        for (int jj = 0; jj < G / 32; ++jj) {
-          const int j = g * (G / 32) + jj;
-#pragma unroll
-          for (int i = 0; i < WMF; ++i) {
-            const uint4 t = *reinterpret_cast<const uint4*>(At + i * 32 * kBlock + 16 * ((2 * j + h) ^ swz));
-            acc[i] = __builtin_amdgcn_mfma_i32_32x32x32_i8(
-                v4i{(int)t.x, (int)t.y, (int)t.z, (int)t.w}, w[j], jj ? acc[i] : zero, 0, 0, 0);
-          }
-        }
-        const float s = frag[S].s.scale(g);
-#pragma unroll
-        for (int i = 0; i < WMF; ++i)
-#pragma unroll
-          for (int v = 0; v < 16; ++v) sum[i][v] = fmaf((float)acc[i][v], s, sum[i][v]);
+    for (int j = 0; j < 4; ++j) {
+      if constexpr (!ZEROS) {
+        w[j] = v4i{low16(u[j]), high16(u[j]), low16(u[4 + j]), high16(u[4 + j])};
+      } else {
+        const uint32_t zz = frag[S].z.zero_bytes(j / (G / 32));
+        w[j] = v4i{low_z(u[j], zz), high_z(u[j], zz), low_z(u[4 + j], zz), high_z(u[4 + j], zz)};
       }
     }
-    wait_vmem<kLoads>();
+    v16i zero;
+#pragma unroll
+    for (int v = 0; v < 16; ++v) zero[v] = 0;
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+      v16i acc[WMF];
+#pragma unroll
+      for (int jj = 0; jj < G / 32; ++jj) {
+        const int j = g * (G / 32) + jj;
+#pragma unroll
+        for (int i = 0; i < WMF; ++i) {
+          const uint4 t = *reinterpret_cast<const uint4*>(At + i * 32 * kBlock + 16 * ((2 * j + h) ^ swz));
+          acc[i] = __builtin_amdgcn_mfma_i32_32x32x32_i8(
+              v4i{(int)t.x, (int)t.y, (int)t.z, (int)t.w}, w[j], jj ? acc[i] : zero, 0, 0, 0);
+        }
+      }
+      // waves whose run has ended add nothing
+      const float s = WK == 1 || b < nb ? frag[S].s.scale(g) : 0.0f;
+#pragma unroll
+      for (int i = 0; i < WMF; ++i)
+#pragma unroll
+        for (int v = 0; v < 16; ++v) sum[i][v] = fmaf((float)acc[i][v], s, sum[i][v]);
+    }
+    wait_vmem<REFILL ? kLoads : 0>();
     __builtin_amdgcn_sched_barrier(0);
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_sched_barrier(0);
   };
   int b = 0;
   for (; b + 3 <= per; b += 3) {
-    step(I0{}, b);
-    step(I1{}, b + 1);
-    step(I2{}, b + 2);
+    step(I0{}, b, std::true_type{});
+    step(I1{}, b + 1, std::true_type{});
+    step(I2{}, b + 2, std::true_type{});
   }
-  if (b < per) step(I0{}, b);
-  if (b + 1 < per) step(I1{}, b + 1);
-  wait_vmem<0>();   // no load may land in LDS after the block has finished
+  wait_vmem<0>();   // the last two stages (no load may land in LDS after the block has ended)
+  lds_sync();
+  if (b < per) step(I0{}, b, std::false_type{});
+  if (b + 1 < per) step(I1{}, b + 1, std::false_type{});
 
   if constexpr (WK > 1) {
     if (wk > 0) {
