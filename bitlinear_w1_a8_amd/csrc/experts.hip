@@ -30,132 +30,6 @@ bool token_wins(int64_t p, int64_t e) { return p <= 32 || p <= e; }
 // slots 18.0 / 18.2, 16 slots 23.7 / 19.8).
 bool few_wins(int64_t p, int64_t e) { return p <= 12 * e; }
 
-// Few rows per expert (decode): up to 16 slots of one expert against 16 RT of
-// its rows per block; the waves split K and add their sums through LDS.  As
-// in the decode kernels of a single matrix, v_mfma_i32_16x16x64_i8 contracts
-// the codes t + 1 and each wave takes the sum of q over its own k off again.
-template <int VEC, int RT, int U, bool GATED>
-__global__ __launch_bounds__(256) void k_experts_rows(const Slots slots,
-                                                      const uint32_t* __restrict__ packed,
-                                                      const float* __restrict__ gamma,
-                                                      const float* __restrict__ gamma2,
-                                                      const int8_t* __restrict__ xq,
-                                                      const float* __restrict__ absmax, int N,
-                                                      int K, int first, float* __restrict__ y,
-                                                      uint16_t* __restrict__ h,
-                                                      int32_t* __restrict__ acc_out) {
-  constexpr int kWaves = 4, kRows = 16 * RT;
-  __shared__ int red[kWaves][RT * 4][64];
-  int expert, p0, p1;
-  if (!find_rows(slots, first + (int)blockIdx.y, 16, expert, p0, p1)) return;
-  const int nrow = p1 - p0;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int qg = lane >> 4, r = lane & 15;
-  const int K16 = K >> 4;
-  const int nchunks = (K16 + 4 * VEC - 1) / (4 * VEC);
-  const int n0 = blockIdx.x * kRows;
-
-  const uint32_t* wrow[RT];
-#pragma unroll
-  for (int rt = 0; rt < RT; ++rt) {
-    const int n = min(n0 + 16 * rt + r, N - 1);     // rows past N are computed, never stored
-    wrow[rt] = packed + ((int64_t)expert * N + n) * K16;
-  }
-  const bool valid = r < nrow;
-  const int8_t* xrow = xq + (int64_t)slot_row(slots, valid ? p0 + r : p0) * K;
-
-  v4i acc[RT];
-  int qs = 0;
-#pragma unroll
-  for (int rt = 0; rt < RT; ++rt) acc[rt] = v4i{0, 0, 0, 0};
-  for (int c0 = wave * U; c0 < nchunks; c0 += kWaves * U) {
-    uint32_t wv[U][RT][VEC], xv[U][4 * VEC];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int wi = (c0 + u) * 4 * VEC + qg * VEC;
-      const bool kvalid = wi < K16;                 // VEC divides K16 when VEC > 1
-#pragma unroll
-      for (int rt = 0; rt < RT; ++rt) {
-        if constexpr (VEC == 4) {
-          const uint4 w4 =
-              kvalid ? *reinterpret_cast<const uint4*>(wrow[rt] + wi) : make_uint4(0, 0, 0, 0);
-          wv[u][rt][0] = w4.x; wv[u][rt][1] = w4.y; wv[u][rt][2] = w4.z; wv[u][rt][3] = w4.w;
-        } else {
-          wv[u][rt][0] = kvalid ? wrow[rt][wi] : 0u;
-        }
-      }
-      const uint4* src = reinterpret_cast<const uint4*>(xrow + (int64_t)wi * 16);
-#pragma unroll
-      for (int v = 0; v < VEC; ++v) {
-        const uint4 x4 = kvalid && valid ? src[v] : make_uint4(0, 0, 0, 0);
-        xv[u][4 * v + 0] = x4.x; xv[u][4 * v + 1] = x4.y;
-        xv[u][4 * v + 2] = x4.z; xv[u][4 * v + 3] = x4.w;
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-#pragma unroll
-      for (int d = 0; d < 4 * VEC; ++d)
-        qs = __builtin_amdgcn_sdot4((int)xv[u][d], 0x01010101, qs, false);
-#pragma unroll
-      for (int v = 0; v < VEC; ++v) {
-        const v4i b = {(int)xv[u][4 * v + 0], (int)xv[u][4 * v + 1], (int)xv[u][4 * v + 2],
-                       (int)xv[u][4 * v + 3]};
-#pragma unroll
-        for (int rt = 0; rt < RT; ++rt) {
-          const uint32_t w = wv[u][rt][v];
-          const v4i a = {(int)codes_of(w, 0), (int)codes_of(w, 1), (int)codes_of(w, 2),
-                         (int)codes_of(w, 3)};
-          acc[rt] = __builtin_amdgcn_mfma_i32_16x16x64_i8(a, b, acc[rt], 0, 0, 0);
-        }
-      }
-    }
-  }
-  qs += __shfl_xor(qs, 16);
-  qs += __shfl_xor(qs, 32);
-#pragma unroll
-  for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-    for (int v = 0; v < 4; ++v) red[wave][rt * 4 + v][lane] = acc[rt][v] - qs;
-  __syncthreads();
-
-  const float g = gamma[expert];
-  auto sum_of = [&](int nl, int tl) {
-    const int i = nl & 15, slot = (nl >> 4) * 4 + (i & 3), ln = (i >> 2) * 16 + tl;
-    int s = 0;
-#pragma unroll
-    for (int w = 0; w < kWaves; ++w) s += red[w][slot][ln];
-    return s;
-  };
-  if constexpr (GATED) {
-    // rows 2i (gate) and 2i + 1 (up) make output n0 / 2 + i
-    const float g2 = gamma2[expert];
-    for (int idx = threadIdx.x; idx < kRows / 2 * nrow; idx += 256) {
-      const int pl = idx % (kRows / 2), tl = idx / (kRows / 2);
-      const int n = n0 + 2 * pl;
-      if (n >= N) continue;
-      const int sg = sum_of(2 * pl, tl), su = sum_of(2 * pl + 1, tl);
-      const int64_t p = p0 + tl;
-      if (acc_out) {
-        acc_out[p * N + n] = sg;
-        acc_out[p * N + n + 1] = su;
-      }
-      const float a = absmax[slot_row(slots, p0 + tl)];
-      h[p * (N >> 1) + (n >> 1)] = gated_relu2_bf16(sg, su, gamma_m(g, a), gamma_m(g2, a));
-    }
-  } else {
-    for (int idx = threadIdx.x; idx < kRows * nrow; idx += 256) {
-      const int nl = idx % kRows, tl = idx / kRows;
-      const int n = n0 + nl;
-      if (n >= N) continue;
-      const int s = sum_of(nl, tl);
-      const int64_t o = (int64_t)(p0 + tl) * N + n;
-      if (acc_out) acc_out[o] = s;
-      y[o] = (float)s * out_scale(g, absmax[slot_row(slots, p0 + tl)]);
-    }
-  }
-}
-
 enum Mode { kInt8 = 0, kBf16 = 1, kF32 = 2 };
 
 typedef __attribute__((address_space(3))) void* lds_ptr_t;
@@ -213,16 +87,20 @@ __device__ __forceinline__ v4i operand(uint32_t w) {
 // 16 bytes that spread the rows of one operand read over the banks.
 __host__ __device__ constexpr int few_stride(int k) { return ((k + 255) & ~255) + 16; }
 
-// A few rows per expert (decode batches): up to R slots of one expert, their
-// int8 rows whole in LDS, against 16 weight rows per wave over all of K.  No
-// wave waits for another after the rows are staged and none adds to another's
-// sums, so a wave is one run of loads: its first U chunks (256 k of 16 rows, 1
-// KiB) are in flight while the rows are staged.  K % 64 == 0.
+// A few rows per expert (decode batches): up to R <= 16 slots of one expert,
+// their int8 rows whole in LDS, against 16 weight rows per wave over all of K
+// on v_mfma_i32_16x16x64_i8, which contracts the codes t + 1; each row's sum of
+// q comes off at the end.  No wave waits for another after the rows are staged
+// and none adds to another's sums, so a wave is one run of loads: its first U
+// chunks (256 k of 16 rows, 1 KiB) are in flight while the rows are staged.
+// Bound by the weight stream (gated, 33 tokens, 6 of 64 experts each, 2560 -> 2 x 1000:
+// 79 MB in 14.5 us, 5.4 TB/s; one token, 8 experts, 2560 -> 2 x 1024: 7.1 us, of
+// which the launch and three dependent loads are more than half).
 // MODE kBf16, kF32: step A1 happens in the staging (every block of an expert
 // repeats it: for batches of a few tokens, whose own launch would cost more),
 // and the first block of an expert writes the codes and absmax of the tokens
 // whose first rank it has.
-template <int MODE, bool GATED, int U>
+template <int MODE, bool GATED, int U, int Q>
 __global__ __launch_bounds__(512) void k_experts_few(const Slots slots,
                                                      const uint32_t* __restrict__ packed,
                                                      const float* __restrict__ gamma,
@@ -242,7 +120,7 @@ __global__ __launch_bounds__(512) void k_experts_few(const Slots slots,
   const int tid = threadIdx.x, lane = tid & 63, nthreads = blockDim.x;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), nwaves = nthreads >> 6;
   const int qg = lane >> 4, r = lane & 15;
-  const int K64 = K >> 6, nchunks = (K64 + 3) >> 2, stride = few_stride(K);
+  const int K16 = K >> 4, nchunks = (K + 255) >> 8, stride = few_stride(K);
   const int n0 = (blockIdx.x * nwaves + wave) * 16;
 
   // The rows first, straight into LDS, then the weights: loads come back in
@@ -261,14 +139,13 @@ __global__ __launch_bounds__(512) void k_experts_few(const Slots slots,
                                          (lds_ptr_t)(land + i * land_stride + b), 16, 0, 0);
   }
   __builtin_amdgcn_sched_barrier(0);
-  // weights: lane (qg, r) takes 64 k (16 bytes) of row r per chunk; in a short
-  // last chunk the lanes past the row's end load its last 16 bytes again and
-  // meet zero activations
+  // weights: lane (qg, r) takes 64 k (16 bytes) of row r per chunk; rows past N
+  // are computed, never stored
   const int n = min(n0 + r, N - 1);
-  const uint4* wrow = reinterpret_cast<const uint4*>(packed) + ((int64_t)expert * N + n) * K64;
+  const uint32_t* wrow = packed + ((int64_t)expert * N + n) * K16;
   uint4 w[U];
 #pragma unroll
-  for (int u = 0; u < U; ++u) w[u] = wrow[min(4 * min(u, nchunks - 1) + qg, K64 - 1)];
+  for (int u = 0; u < U; ++u) w[u] = load_quad<Q>(wrow, 16 * min(u, nchunks - 1) + 4 * qg, K16);
   __builtin_amdgcn_sched_barrier(0);
   if (tid < 16) qsum[tid] = amax[tid] = 0;
   wait_vmem<U>();                                   // this wave's rows are in LDS
@@ -277,14 +154,14 @@ __global__ __launch_bounds__(512) void k_experts_few(const Slots slots,
     for (int i = wave; i < nrow; i += nwaves) {
       uint4* row = reinterpret_cast<uint4*>(xs + i * stride);
       int s = 0;
-      for (int v = lane; v < 4 * K64; v += 64) {
+      for (int v = lane; v < K16; v += 64) {
         const uint4 q = row[v];
         s = __builtin_amdgcn_sdot4((int)q.x, 0x01010101, s, false);
         s = __builtin_amdgcn_sdot4((int)q.y, 0x01010101, s, false);
         s = __builtin_amdgcn_sdot4((int)q.z, 0x01010101, s, false);
         s = __builtin_amdgcn_sdot4((int)q.w, 0x01010101, s, false);
       }
-      if (4 * K64 + lane < 16 * nchunks) row[4 * K64 + lane] = make_uint4(0, 0, 0, 0);
+      if (K16 + lane < 16 * nchunks) row[K16 + lane] = make_uint4(0, 0, 0, 0);   // fewer than 16
       s = wave_sum_i(s);
       if (lane == 0) qsum[i] = s;
     }
@@ -330,18 +207,16 @@ __global__ __launch_bounds__(512) void k_experts_few(const Slots slots,
     for (int u = 0; u < U; ++u) {
       if (c0 + u >= nchunks) break;
       const uint4* xv = reinterpret_cast<const uint4*>(xrow + (c0 + u) * 256);
-      const uint32_t word[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
+      const uint4 p = settle<Q>(w[u], 16 * (c0 + u) + 4 * qg, K16);
+      const uint32_t word[4] = {p.x, p.y, p.z, p.w};
+      // the buffer's next chunk at once
+      if (c0 + U + u < nchunks) w[u] = load_quad<Q>(wrow, 16 * (c0 + U + u) + 4 * qg, K16);
 #pragma unroll
       for (int v = 0; v < 4; ++v) {
         const uint4 q = xv[v];
         acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(
             operand(word[v]), v4i{(int)q.x, (int)q.y, (int)q.z, (int)q.w}, acc, 0, 0, 0);
       }
-    }
-    if (c0 + U < nchunks) {
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-        w[u] = wrow[min(4 * min(c0 + U + u, nchunks - 1) + qg, K64 - 1)];
     }
   }
 
@@ -374,9 +249,8 @@ __global__ __launch_bounds__(512) void k_experts_few(const Slots slots,
 // 16 outputs, each of its k slots a team of `team` waves that split K.  A team
 // quantises its slot's row (step A1; every block of the token repeats it) and
 // contracts it with the slot's expert; the teams' exact sums meet in LDS, and
-// the rescale and the sum over the ranks follow in order.  K % 64 == 0,
-// k * team <= 16.
-template <int MODE, int U>
+// the rescale and the sum over the ranks follow in order.  k * team <= 16.
+template <int MODE, int U, int Q>
 __global__ __launch_bounds__(1024) void k_experts_token(const Slots slots,
                                                         const int32_t* __restrict__ slot_of,
                                                         const float* __restrict__ weights, int topk,
@@ -393,7 +267,7 @@ __global__ __launch_bounds__(1024) void k_experts_token(const Slots slots,
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int qg = lane >> 4, r = lane & 15;
   const int t = blockIdx.y, j = wave / team, part = wave - j * team;
-  const int K64 = K >> 6, nchunks = (K64 + 3) >> 2, stride = few_stride(K);
+  const int K16 = K >> 4, nchunks = (K + 255) >> 8, stride = few_stride(K);
   const int per = (nchunks + team - 1) / team, c0 = part * per, c1 = min(c0 + per, nchunks);
   const int n0 = blockIdx.x * 16;
   if (tid < 256) (&tile[0][0])[tid] = 0;
@@ -409,8 +283,7 @@ __global__ __launch_bounds__(1024) void k_experts_token(const Slots slots,
   const int row = slots.k ? t : max(slot, 0);
   constexpr int kBytes = MODE == kBf16 ? 2 : 4;
   const void* xrow = static_cast<const unsigned char*>(x) + (int64_t)row * K * kBytes;
-  const uint4* wrow = reinterpret_cast<const uint4*>(packed) +
-                      ((int64_t)expert * N + min(n0 + r, N - 1)) * K64;
+  const uint32_t* wrow = packed + ((int64_t)expert * N + min(n0 + r, N - 1)) * K16;
   const bool live = slot >= 0 && c0 < c1;               // wave-uniform
   // the row before the weights, as above; its first U chunks stay in registers
   Raw4<MODE> xr[U];
@@ -424,7 +297,8 @@ __global__ __launch_bounds__(1024) void k_experts_token(const Slots slots,
     }
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int u = 0; u < U; ++u) w[u] = wrow[min(4 * min(c0 + u, c1 - 1) + qg, K64 - 1)];
+    for (int u = 0; u < U; ++u)
+      w[u] = load_quad<Q>(wrow, 16 * min(c0 + u, c1 - 1) + 4 * qg, K16);
   }
   const float g = gamma[expert];
   lds_sync();
@@ -479,18 +353,15 @@ __global__ __launch_bounds__(1024) void k_experts_token(const Slots slots,
       for (int u = 0; u < U; ++u) {
         if (b0 + u >= c1) break;
         const uint4* xv = reinterpret_cast<const uint4*>(xq + (b0 + u) * 256);
-        const uint32_t word[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
+        const uint4 p = settle<Q>(w[u], 16 * (b0 + u) + 4 * qg, K16);
+        const uint32_t word[4] = {p.x, p.y, p.z, p.w};
+        if (b0 + U + u < c1) w[u] = load_quad<Q>(wrow, 16 * (b0 + U + u) + 4 * qg, K16);
 #pragma unroll
         for (int v = 0; v < 4; ++v) {
           const uint4 b = xv[v];
           acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(
               operand(word[v]), v4i{(int)b.x, (int)b.y, (int)b.z, (int)b.w}, acc, 0, 0, 0);
         }
-      }
-      if (b0 + U < c1) {
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-          w[u] = wrow[min(4 * min(b0 + U + u, c1 - 1) + qg, K64 - 1)];
       }
     }
     if (r == 0) {
@@ -546,7 +417,7 @@ size_t few_lds(int64_t k, int rows, int mode) {
   return (size_t)rows * (few_stride((int)k) + (mode == kInt8 ? 0 : mode == kBf16 ? 2 * k : 4 * k));
 }
 bool few_fits(int64_t k, int rows, int mode) {
-  return k % 64 == 0 && few_lds(k, rows, mode) <= (size_t)kMaxLds;
+  return few_lds(k, rows, mode) <= (size_t)kMaxLds;
 }
 
 template <int MODE, bool GATED>
@@ -570,8 +441,12 @@ hipError_t launch_few(const Slots& s, const uint8_t* packed, const float* gamma,
     }
     return e;
   };
-  if (k <= 1024) return go(Kernel<k_experts_few<MODE, GATED, 4>>{});
-  return go(Kernel<k_experts_few<MODE, GATED, 10>>{});
+  if (k < 64) return go(Kernel<k_experts_few<MODE, GATED, 4, kWords>>{});
+  if (k % 64)
+    return k <= 1024 ? go(Kernel<k_experts_few<MODE, GATED, 4, kShort>>{})
+                     : go(Kernel<k_experts_few<MODE, GATED, 10, kShort>>{});
+  return k <= 1024 ? go(Kernel<k_experts_few<MODE, GATED, 4, kWhole>>{})
+                   : go(Kernel<k_experts_few<MODE, GATED, 10, kWhole>>{});
 }
 
 template <int MODE>
@@ -590,27 +465,9 @@ hipError_t launch_token(const Slots& s, const bl_routing& r, const uint8_t* pack
                                                   x, (int)n, (int)k, y, xq, absmax);
     return hipGetLastError();
   };
-  return go(Kernel<k_experts_token<MODE, 4>>{});
-}
-
-template <bool GATED>
-hipError_t launch_rows(const Slots& s, const uint8_t* packed, const float* gamma,
-                       const float* gamma2, const int8_t* xq, const float* absmax, int64_t n,
-                       int64_t k, float* y, uint16_t* h, int32_t* acc, hipStream_t stream) {
-  const auto* w = reinterpret_cast<const uint32_t*>(packed);
-  const int64_t blocks = row_blocks(s.P, s.E, 16);
-  for (int64_t b = 0; b < blocks; b += 65535) {     // grid.y holds at most 65535 blocks
-    const dim3 grid((unsigned)((n + 15) / 16), (unsigned)std::min<int64_t>(blocks - b, 65535));
-    if (k % 64 == 0)
-      k_experts_rows<4, 1, 2, GATED><<<grid, 256, 0, stream>>>(s, w, gamma, gamma2, xq, absmax,
-                                                               (int)n, (int)k, (int)b, y, h, acc);
-    else
-      k_experts_rows<1, 1, 4, GATED><<<grid, 256, 0, stream>>>(s, w, gamma, gamma2, xq, absmax,
-                                                               (int)n, (int)k, (int)b, y, h, acc);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-  }
-  return hipSuccess;
+  if (k < 64) return go(Kernel<k_experts_token<MODE, 4, kWords>>{});
+  return k % 64 ? go(Kernel<k_experts_token<MODE, 4, kShort>>{})
+                : go(Kernel<k_experts_token<MODE, 4, kWhole>>{});
 }
 
 // Steps A2 + A3 of int8 rows by the kernel for their number and length.
@@ -619,14 +476,16 @@ hipError_t launch_products(const Slots& s, int64_t x_rows, const uint8_t* packed
                            const float* gamma, const float* gamma2, const int8_t* xq,
                            const float* absmax, int64_t n, int64_t k, float* y, uint16_t* h,
                            int32_t* acc, hipStream_t stream) {
-  const bool tiled = k % 64 == 0 && x_rows * k < (int64_t(1) << 31) &&
-                     n * (k / 16) < (int64_t(1) << 31);
-  if (few_fits(k, 16, kInt8) && (few_wins(s.P, s.E) || !tiled))
-    return launch_few<kInt8, GATED>(s, packed, gamma, gamma2, xq, absmax, n, k, 16, y, h, acc,
-                                    nullptr, nullptr, stream);
-  if (tiled)
+  // the tiled kernel's 32-bit offsets, and blocks of 256 threads in a grid
+  const bool tiled = k >= 64 && x_rows * k < (int64_t(1) << 31) &&
+                     n * (k / 16) < (int64_t(1) << 31) &&
+                     (n + 127) / 128 * row_blocks(s.P, s.E, 32) < (int64_t(1) << 24) - 8;
+  if (tiled && !few_wins(s.P, s.E))
     return launch_gemm_experts(s, packed, gamma, gamma2, xq, absmax, n, k, y, h, acc, stream);
-  return launch_rows<GATED>(s, packed, gamma, gamma2, xq, absmax, n, k, y, h, acc, stream);
+  int rows = 16;                       // as many as LDS holds; one of the longest fits
+  while (!few_fits(k, rows, kInt8)) rows /= 2;
+  return launch_few<kInt8, GATED>(s, packed, gamma, gamma2, xq, absmax, n, k, rows, y, h, acc,
+                                  nullptr, nullptr, stream);
 }
 
 }  // namespace

@@ -274,7 +274,8 @@ __device__ __align__(16) int8_t kZeroPage[1024];
 // the half step falls in the last part.
 // EXPERTS: routed rows.  A row block holds slots of one expert; the block
 // finds them and the expert's matrix and gammas from the routing, gathers its
-// activation rows through it and writes by slot.  T is not used.
+// activation rows through it and writes by slot.  T is not used.  With TAIL, K
+// is any multiple of 16 that is not one of 128 (register weights only).
 template <int WAVES, int WAVES_M, int WMF, int WNF, int STAGES, bool SPLIT, bool GATED,
           int WBITS = 2, bool RS = false, bool TAIL = false, bool EXPERTS = false>
 __global__ __launch_bounds__(WAVES * 64) void k_gemm_lds(const uint32_t* __restrict__ packed,
@@ -294,6 +295,7 @@ __global__ __launch_bounds__(WAVES * 64) void k_gemm_lds(const uint32_t* __restr
   static_assert(!(SPLIT && GATED), "the gated epilogue needs whole sums");
   static_assert(!(TAIL && WBITS != 2), "a half last K step: two-bit kernels");
   static_assert(!(EXPERTS && (SPLIT || RS || WBITS != 2)), "experts: whole sums of two-bit weights");
+  static_assert(!EXPERTS || (BL_GEMM_BREG != 0 && WAVES_M == 1), "experts: register weights");
   constexpr int NT = WAVES * 64;
   constexpr int WAVES_N = WAVES / WAVES_M;
   constexpr int BM = WAVES_M * 32 * WMF, BN = WAVES_N * 32 * WNF;
@@ -462,8 +464,13 @@ __global__ __launch_bounds__(WAVES * 64) void k_gemm_lds(const uint32_t* __restr
       // the step's second half (h = 1) past the row end: the first half again
       const uint32_t back = TAIL && k0 + 64u * h_of_lane >= (uint32_t)K ? 4u : 0u;
 #pragma unroll
-      for (int j = 0; j < WNF; ++j)
-        breg[S][j] = *reinterpret_cast<const uint4*>(packed + (roff[j] + (k0 >> 4) - back));
+      for (int j = 0; j < WNF; ++j) {
+        if constexpr (EXPERTS && TAIL)     // any K % 16 == 0
+          breg[S][j] = load_quad<kShort>(packed + (roff[j] - 4u * h_of_lane),
+                                       (int)((k0 >> 4) + 4u * h_of_lane), KW);
+        else
+          breg[S][j] = *reinterpret_cast<const uint4*>(packed + (roff[j] + (k0 >> 4) - back));
+      }
     } else {
       unsigned char* Bs = bbuf(stage_c);
       const uint32_t back = TAIL && k0 + 64u * (lane & 1) >= (uint32_t)K ? 4u : 0u;
@@ -546,7 +553,9 @@ __global__ __launch_bounds__(WAVES * 64) void k_gemm_lds(const uint32_t* __restr
     uint4 bw[WNF];
 #pragma unroll
     for (int j = 0; j < WNF; ++j) {
-      if constexpr (kBReg) bw[j] = breg[S][j];
+      if constexpr (kBReg && EXPERTS && TAIL)
+        bw[j] = settle<kShort>(breg[S][j], (int)(((kbase + (uint32_t)kt * BK) >> 4) + 4u * h_of_lane), KW);
+      else if constexpr (kBReg) bw[j] = breg[S][j];
       else bw[j] = *reinterpret_cast<const uint4*>(Bt + j * 32 * kBRow);
     }
 #pragma unroll

@@ -168,7 +168,13 @@ GATED = [(1, 8, 2, 40, 256, "bf16", "normal"), (1, 64, 8, 1024, 2560, "bf16", "n
          (40, 3, 1, 64, 192, "f32", "equal"), (90, 8, 2, 300, 640, "bf16", "masked"),
          (300, 5, 2, 77, 256, "f32", "normal"), (257, 16, 4, 130, 1088, "bf16", "masked"),
          (700, 4, 3, 520, 384, "bf16", "normal"), (1200, 2, 1, 33, 128, "f32", "normal"),
-         (64, 16, 2, 96, 4096, "bf16", "empty"), (1000, 64, 8, 200, 448, "bf16", "ties")]
+         (64, 16, 2, 96, 4096, "bf16", "empty"), (1000, 64, 8, 200, 448, "bf16", "ties"),
+         # long rows (fewer of them in LDS at a time), many rows of odd lengths,
+         # more experts than lanes
+         (40, 4, 2, 33, 16400, "bf16", "normal"), (3, 3, 2, 9, 131072, "bf16", "normal"),
+         (20, 2, 1, 17, 40000, "f32", "normal"), (400, 3, 2, 70, 272, "bf16", "masked"),
+         (2, 4, 2, 20, 8208, "f32", "normal"), (50, 200, 3, 40, 256, "bf16", "masked"),
+         (300, 1000, 4, 24, 128, "bf16", "ties"), (4, 1024, 8, 16, 80, "f32", "normal")]
 
 
 @pytest.mark.parametrize("t,e,k,n,kk,dtype,kind", GATED,
@@ -205,7 +211,11 @@ LINEAR = [(1, 8, 2, 40, 256, "bf16", "normal"), (1, 64, 8, 2560, 1024, "bf16", "
           (300, 5, 2, 154, 256, "f32", "normal"), (257, 16, 4, 260, 1088, "bf16", "masked"),
           (700, 4, 3, 1040, 384, "bf16", "normal"), (1200, 2, 1, 66, 128, "f32", "normal"),
           (64, 16, 2, 192, 4096, "bf16", "empty"), (1000, 64, 8, 400, 448, "bf16", "ties"),
-          (2, 6, 2, 96, 6912, "bf16", "normal")]
+          (2, 6, 2, 96, 6912, "bf16", "normal"),
+          (40, 4, 2, 33, 16400, "bf16", "normal"), (2, 3, 1, 9, 131072, "bf16", "normal"),
+          (1, 4, 4, 18, 36880, "f32", "normal"), (400, 3, 2, 70, 272, "bf16", "masked"),
+          (50, 200, 3, 40, 256, "bf16", "masked"), (300, 1000, 4, 24, 128, "bf16", "ties"),
+          (4, 1024, 8, 17, 80, "f32", "normal"), (6, 64, 17, 30, 96, "bf16", "normal")]
 
 
 @pytest.mark.parametrize("x_rows", ["slots", "tokens"])
