@@ -84,7 +84,7 @@ bl_status bitlinear_gated_relu2_experts(const bl_routing* routing, const void* x
     return fail(BL_ERR_DTYPE, "%s: unknown x_dtype %d", fn, x_dtype);
   if (bl_status rc = check_counts(fn, r.T, r.k, r.E)) return rc;
   if (bl_status rc = check_k(fn, K)) return rc;
-  if (N < 1 || 2 * N > kMaxN || 2 * N * K > kMaxNK / r.E || r.T * r.k > kMaxTN / (2 * N))
+  if (N < 1 || N > kMaxN / 2 || 2 * N * K > kMaxNK / r.E || r.T * r.k > kMaxTN / (2 * N))
     return fail(BL_ERR_SHAPE, "%s: N=%lld out of range", fn, (long long)N);
   if (!aligned(x, 16) || !aligned(packed_gu, 16) || !aligned(xq, 16) || !aligned(gamma_gate, 4) ||
       !aligned(gamma_up, 4) || !aligned(absmax, 4) || !aligned(h, 2) || !aligned(acc, 4) ||

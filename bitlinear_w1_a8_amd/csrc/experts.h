@@ -58,7 +58,8 @@ __device__ __forceinline__ int slot_row(const Slots& s, int p) {
 
 // Block `c` of `rows` slots each, counted over the experts in order: its
 // expert and slots p0 .. p1 - 1 (all in [0, P)), or false when there are
-// fewer.  Called by whole waves, with the same result in each.
+// fewer, or when the counts of overlapping experts pass 32 bits.  Called by
+// whole waves, with the same result in each.
 __device__ __forceinline__ bool find_rows(const Slots& s, int c, int rows, int& expert, int& p0,
                                           int& p1) {
   const int lane = threadIdx.x & 63;
@@ -79,14 +80,15 @@ __device__ __forceinline__ bool find_rows(const Slots& s, int c, int rows, int& 
     }
     const int total = __builtin_amdgcn_readlane(sum, 63);
     if (c < seen + total) {
-      const int at = __builtin_ctzll(__ballot(seen + sum > c));
+      const unsigned long long reach = __ballot(seen + sum > c);
+      const int at = reach ? __builtin_ctzll(reach) : 0;
       const int first = __builtin_amdgcn_readlane(seen + sum - n, at);
       lo = __builtin_amdgcn_readlane(lo, at);
       hi = __builtin_amdgcn_readlane(hi, at);
       expert = base + at;
       p0 = lo + (c - first) * rows;
       p1 = min(p0 + rows, hi);
-      return true;
+      return reach != 0 && expert < s.E && p0 >= lo && p0 < hi;
     }
     seen += total;
   }

@@ -411,6 +411,18 @@ __global__ __launch_bounds__(256) void k_experts_combine(const float* __restrict
   }
 }
 
+// Step A1 of any number of rows.  A launch has fewer than 2^32 threads and a
+// row takes up to 1024 of them, so 2^21 rows go at a time.
+hipError_t quant_rows(const void* x, int bf16, int64_t rows, int64_t k, int8_t* xq, float* absmax,
+                      hipStream_t stream) {
+  constexpr int64_t kMost = int64_t(1) << 21;
+  hipError_t e = hipSuccess;
+  for (int64_t r = 0; e == hipSuccess && r < rows; r += kMost)
+    e = launch_quant(static_cast<const unsigned char*>(x) + r * k * (bf16 ? 2 : 4), bf16,
+                     std::min(rows - r, kMost), k, xq + r * k, absmax + r, nullptr, stream);
+  return e;
+}
+
 // LDS of k_experts_few for R rows: the int8 rows, and the raw ones that they
 // are made from.
 size_t few_lds(int64_t k, int rows, int mode) {
@@ -500,7 +512,7 @@ hipError_t launch_gated_experts(const bl_routing& r, const void* x, int bf16, co
     return f(s, packed, gamma_gate, gamma_up, x, nullptr, n, k, kFewTokens, nullptr, h, acc, xq,
              absmax, stream);
   }
-  hipError_t e = launch_quant(x, bf16, r.T, k, xq, absmax, nullptr, stream);
+  hipError_t e = quant_rows(x, bf16, r.T, k, xq, absmax, stream);
   if (e != hipSuccess) return e;
   return launch_products<true>(s, r.T, packed, gamma_gate, gamma_up, xq, absmax, n, k, nullptr, h,
                                acc, stream);
@@ -524,7 +536,7 @@ hipError_t launch_linear_experts(const bl_routing& r, const void* x, int bf16, i
     e = f(s, packed, gamma, nullptr, x, nullptr, n, k, kFewTokens, out, nullptr, acc, xq, absmax,
           stream);
   } else {
-    e = launch_quant(x, bf16, rows, k, xq, absmax, nullptr, stream);
+    e = quant_rows(x, bf16, rows, k, xq, absmax, stream);
     if (e != hipSuccess) return e;
     e = launch_products<false>(s, rows, packed, gamma, nullptr, xq, absmax, n, k, out, nullptr,
                                acc, stream);

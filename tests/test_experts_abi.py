@@ -95,7 +95,8 @@ def _gated(lib, desc=None, x=A16, dt=1, packed=A16, g=A16, u=A16, n=16, k=64, h=
     (dict(u=None), BL_ERR_NULL), (dict(h=None), BL_ERR_NULL), (dict(xq=None), BL_ERR_NULL),
     (dict(absmax=None), BL_ERR_NULL), (dict(dt=2), BL_ERR_DTYPE), (dict(k=40), BL_ERR_SHAPE),
     (dict(k=0), BL_ERR_SHAPE), (dict(n=0), BL_ERR_SHAPE), (dict(n=(1 << 25) + 1), BL_ERR_SHAPE),
-    (dict(n=1 << 25, k=131072), BL_ERR_SHAPE), (dict(x=A16 + 8), BL_ERR_ALIGN),
+    (dict(n=1 << 25, k=131072), BL_ERR_SHAPE), (dict(n=(1 << 62) + 1), BL_ERR_SHAPE),
+    (dict(x=A16 + 8), BL_ERR_ALIGN),
     (dict(packed=A16 + 8), BL_ERR_ALIGN), (dict(xq=A16 + 4), BL_ERR_ALIGN), (dict(h=A_ODD), BL_ERR_ALIGN),
     (dict(acc=A16 + 2), BL_ERR_ALIGN), (dict(absmax=A16 + 1), BL_ERR_ALIGN)])
 def test_gated_refusals(lib, kw, code):

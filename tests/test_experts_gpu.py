@@ -67,6 +67,9 @@ def scores(t, e, seed, kind):
     elif kind == "lowest":
         x[rng.random((t, e)) < 0.8] = np.finfo(np.float32).min
     x = x.astype(np.float32)
+    if kind == "infinite":
+        x[rng.random((t, e)) < 1.5 / e] = np.inf
+        x[:, 0] = NINF
     if kind == "masked":
         x[rng.random((t, e)) < 0.5] = NINF
         x[rng.random(t) < 0.3] = NINF
@@ -102,7 +105,8 @@ ROUTES = [(1, 1, 1, "normal"), (1, 64, 8, "normal"), (1, 1024, 32, "normal"), (2
           (3, 64, 8, "empty"), (7, 33, 4, "masked"), (63, 65, 6, "ties"), (64, 128, 8, "equal"),
           (65, 128, 8, "masked"), (64, 3, 3, "zeros"), (200, 256, 8, "lowest"), (129, 257, 2, "wide"),
           (1000, 60, 6, "normal"), (4161, 16, 1, "ties"), (300, 8, 8, "masked"), (70, 1000, 9, "ties"),
-          (100, 64, 32, "masked"), (128, 7, 2, "empty")]
+          (100, 64, 32, "masked"), (128, 7, 2, "empty"), (5, 40, 6, "infinite"), (90, 700, 12, "infinite"),
+          (2100, 300, 5, "masked")]
 
 
 @pytest.mark.parametrize("share", ["chosen", "all"])
@@ -397,6 +401,53 @@ def test_rows_past_32_bits(bl, combine):
     assert np.all(np.abs(got - want) <= 6 * U * np.abs(want))
     del y
     torch.cuda.empty_cache()
+
+
+def test_more_rows_than_a_launch_takes(bl):
+    """2^26 + 9 slots of K = 16, one row of x each: more than 2^32 threads of step A1."""
+    t, k, e, kk = (1 << 26) // 8 + 1, 8, 8, 16
+    p = t * k
+    tern, packed, gam = weights(np.random.default_rng(5), e, 4, kk)
+    gen = torch.Generator("cuda").manual_seed(3)
+    x = torch.randn(p, kk, device="cuda", generator=gen, dtype=torch.bfloat16)
+    r = bl.route_experts(torch.randn(t, e, device="cuda", generator=gen), k)   # every expert: t slots each
+    y = bl.linear_experts(x, packed, dev(gam), r, combine=False)
+    for i in (0, 3, e - 1):
+        at = slice(i * t, (i + 1) * t)
+        rows = torch.cat([torch.arange(70), torch.arange(t - 70, t), torch.arange(0, t, 99991)]).cuda()
+        q, a = bl.quant_act(x[at][rows].contiguous())[:2]
+        want = bl.forward(packed[i].contiguous(), dev(gam[i:i + 1]), q, a, 4)
+        assert torch.equal(y[at][rows], want[0] if isinstance(want, tuple) else want)
+    del x, y, r
+    torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("t,e,k,kk", [(2, 9, 3, 64), (40, 9, 3, 80), (600, 9, 3, 128), (600, 70, 2, 64)])
+def test_routing_of_anything_stays_in_bounds(bl, t, e, k, kk):
+    """Arrays that the router would not write: the calls end and nothing beside
+    the outputs changes."""
+    n = 40
+    rng = np.random.default_rng(t + e)
+    def some(shape):
+        v = rng.integers(-2 ** 31, 2 ** 31, shape)
+        return dev(np.where(rng.random(shape) < 0.5, v, rng.integers(-2, t * k + 2, shape)).astype(np.int32))
+    r = bl.Routing(None, torch.ones(t, k, device="cuda"), some(e + 1), some(t * k), some((t, k)))
+    _, gu, gam = weights(rng, e, 2 * n, kk)
+    _, dn, _ = weights(rng, e, n, kk)
+    x = activations(t, kk, 1, "bf16")[0]
+    xs = activations(t * k, kk, 2, "bf16")[0]
+    def padded(rows, dtype):
+        whole = torch.full((rows + 2, n), 7, dtype=dtype, device="cuda")
+        return whole, whole[1:-1]
+    # an output begins one row in: 80 or 160 bytes, a multiple of 16
+    h_all, h = padded(t * k, torch.bfloat16)
+    bl.gated_relu2_experts(x, gu, dev(gam), dev(gam), r, out=h)
+    y_all, y = padded(t, torch.float32)
+    bl.linear_experts(xs, dn, dev(gam), r, out=y)
+    s_all, s = padded(t * k, torch.float32)
+    bl.linear_experts(x, dn, dev(gam), r, combine=False, x_rows="tokens", out=s)
+    for whole in (h_all, y_all, s_all):
+        assert bool((whole[0] == 7).all()) and bool((whole[-1] == 7).all())
 
 
 # ------------------------------------------------------------------ refusals of the binding
