@@ -33,7 +33,8 @@ struct Kernel {
 
 // ---------------------------------------------------------------- router (route.hip)
 
-constexpr int kRouteTokens = 64;   // tokens of a block: one bit each in an expert's mask
+constexpr int kOneBlock = 64;      // tokens that one block routes alone: a bit each in an expert's mask
+constexpr int kRouteTokens = 32;   // tokens of a block where there are more
 
 size_t route_workspace_bytes(int64_t t, int64_t e);
 hipError_t launch_route(const void* logits, int bf16, int64_t t, int64_t e, int64_t k, int share,

@@ -9,14 +9,16 @@
 // for rank j.  With a row per token a wave's instructions serve four tokens,
 // and instructions are what bounds this kernel (8192 tokens, 128 experts, k = 8,
 // the whole router: a wave per token with an exponential in every rank 23.5
-// us, this 15.2; 64 tokens 17.1 -> 9.5).
+// us, this 12.6; 64 tokens 17.1 -> 9.5).
 //
-// Slots.  A block takes 64 tokens, whose choice of expert e is one 64-bit
-// mask: a pair's place among its expert's pairs of the block is the number of
+// Slots.  A block takes up to 64 tokens, whose choices of expert e are one
+// 64-bit mask: a pair's place among its expert's pairs of the block is the number of
 // mask bits below its token.  The masks are integers set by or, so nothing
 // depends on an order of execution.  Up to 64 tokens one block does
-// everything; more take a second kernel that turns the blocks' counts into
-// starts (one wave per expert) and a third that writes the slots.
+// everything; more are chosen 32 per block (64 leave half the CUs idle at 8192
+// tokens: 15.2 -> 14.0 us), a last kernel writes the slots, and where the counts are
+// many one in between turns them into starts (one wave per expert, four counts a
+// lane: 14.0 -> 12.6).
 #include <type_traits>
 
 #include "experts.h"
@@ -26,6 +28,7 @@ namespace {
 
 constexpr int kThreads = 1024;
 constexpr int kWaves = kThreads / 64;
+constexpr int kChooseThreads = 16 * kRouteTokens;   // a row of lanes per token
 constexpr int kMaxE = BITLINEAR_MAX_EXPERTS;
 static_assert(kMaxE <= kThreads, "one thread per expert");
 
@@ -85,11 +88,11 @@ __device__ __forceinline__ int block_scan(int v, int* part, int& total) {
 }
 
 // Top k of one block's tokens; marks each choice in the masks.  k <= LANES.
-template <int LANES, int VPL, bool BF16>
+template <int THREADS, int LANES, int VPL, bool BF16>
 __device__ __forceinline__ void choose(const void* __restrict__ logits, int64_t t0, int nt, int E,
                                        int k, int share, int32_t* __restrict__ ids,
                                        float* __restrict__ weights, unsigned long long* mask) {
-  constexpr int kTeams = kThreads / LANES;
+  constexpr int kTeams = THREADS / LANES;
   const int lane = threadIdx.x % LANES, team = threadIdx.x / LANES;
   auto larger = [](uint32_t a, uint32_t b) { return a > b ? a : b; };
   auto lower = [](int a, int b) { return a < b ? a : b; };
@@ -186,7 +189,7 @@ __global__ __launch_bounds__(kThreads) void k_route_one(const void* __restrict__
   const int e = threadIdx.x;
   mask[e] = 0;
   __syncthreads();
-  choose<LANES, VPL, BF16>(logits, 0, T, E, k, share, ids, weights, mask);
+  choose<kThreads, LANES, VPL, BF16>(logits, 0, T, E, k, share, ids, weights, mask);
   __syncthreads();
   int used;
   const int first = block_scan(__builtin_popcountll(mask[e]), part, used);
@@ -201,19 +204,20 @@ __global__ __launch_bounds__(kThreads) void k_route_one(const void* __restrict__
 // More tokens, first kernel: choices, and each block's count per expert.
 // workspace: counts [E][blocks], then totals [E].
 template <int LANES, int VPL, bool BF16>
-__global__ __launch_bounds__(kThreads) void k_route_choose(const void* __restrict__ logits, int T,
-                                                           int E, int k, int share,
-                                                           int32_t* __restrict__ ids,
-                                                           float* __restrict__ weights,
-                                                           int32_t* __restrict__ counts) {
+__global__ __launch_bounds__(kChooseThreads) void k_route_choose(const void* __restrict__ logits,
+                                                                 int T, int E, int k, int share,
+                                                                 int32_t* __restrict__ ids,
+                                                                 float* __restrict__ weights,
+                                                                 int32_t* __restrict__ counts) {
   __shared__ unsigned long long mask[kMaxE];
-  const int e = threadIdx.x;
-  mask[e] = 0;
+  for (int e = threadIdx.x; e < E; e += kChooseThreads) mask[e] = 0;
   __syncthreads();
   const int t0 = blockIdx.x * kRouteTokens;
-  choose<LANES, VPL, BF16>(logits, t0, min(kRouteTokens, T - t0), E, k, share, ids, weights, mask);
+  choose<kChooseThreads, LANES, VPL, BF16>(logits, t0, min(kRouteTokens, T - t0), E, k, share, ids,
+                                           weights, mask);
   __syncthreads();
-  if (e < E) counts[(int64_t)e * gridDim.x + blockIdx.x] = __builtin_popcountll(mask[e]);
+  for (int e = threadIdx.x; e < E; e += kChooseThreads)
+    counts[(int64_t)e * gridDim.x + blockIdx.x] = __builtin_popcountll(mask[e]);
 }
 
 // Second kernel, one wave per expert: counts -> pairs of the expert in earlier blocks.
@@ -222,15 +226,24 @@ __global__ __launch_bounds__(64) void k_route_starts(int32_t* __restrict__ count
   const int lane = threadIdx.x;
   int32_t* c = counts + (int64_t)blockIdx.x * blocks;
   int before = 0;
-  for (int b = 0; b < blocks; b += 64) {
-    const int v = b + lane < blocks ? c[b + lane] : 0;
-    int s = v;
+  for (int b0 = 0; b0 < blocks; b0 += 256) {
+    const int b = b0 + 4 * lane;
+    int v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = b + i < blocks ? c[b + i] : 0;
+    const int own = v[0] + v[1] + v[2] + v[3];
+    int s = own;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
       const int o = __shfl_up(s, d);
       if (lane >= d) s += o;
     }
-    if (b + lane < blocks) c[b + lane] = before + s - v;
+    int at = before + s - own;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (b + i < blocks) c[b + i] = at;
+      at += v[i];
+    }
     before += __builtin_amdgcn_readlane(s, 63);
   }
   if (lane == 0) totals[blockIdx.x] = before;
@@ -295,14 +308,16 @@ __global__ __launch_bounds__(kThreads) void k_route_place(const int32_t* __restr
 
 }  // namespace
 
-// Counts (blocks times experts) up to which every block of the last kernel adds
-// them up itself instead of a kernel in between (k = 8: 64 experts, 8192 tokens 10.6
-// against 11.7 us; 128 experts, 8192 tokens 15.8 / 15.2).
-constexpr int64_t kSumMost = 8192;
+// Every block of the last kernel adds up the counts itself, 64 experts by 16
+// blocks a round, where that takes few rounds; else a kernel in between does
+// (8 rounds, 4096 tokens x 64 experts 9.5 against 10.1 us, 2048 x 128 11.1 / 11.7;
+// 16 rounds, 8192 x 64 11.3 / 10.4, 4096 x 128 12.8 / 12.0; 1 round, 256 x 128
+// 10.1 / 11.5).
+bool sum_wins(int64_t blocks, int64_t e) { return (blocks + 15) / 16 * ((e + 63) / 64) <= 8; }
 
 size_t route_workspace_bytes(int64_t t, int64_t e) {
   const int64_t blocks = (t + kRouteTokens - 1) / kRouteTokens;
-  return blocks <= 1 ? 0 : (size_t)((blocks + 1) * e) * sizeof(int32_t);
+  return t <= kOneBlock ? 0 : (size_t)((blocks + 1) * e) * sizeof(int32_t);
 }
 
 hipError_t launch_route(const void* logits, int bf16, int64_t t, int64_t e, int64_t k, int share,
@@ -312,12 +327,12 @@ hipError_t launch_route(const void* logits, int bf16, int64_t t, int64_t e, int6
   auto go = [&](auto lanes, auto vpl, auto bf) {
     constexpr int L = decltype(lanes)::value, V = decltype(vpl)::value;
     constexpr bool B = decltype(bf)::value;
-    if (blocks == 1)
+    if (t <= kOneBlock)
       k_route_one<L, V, B><<<1, kThreads, 0, stream>>>(logits, (int)t, (int)e, (int)k, share, ids,
                                                        weights, offsets, pairs, slots);
     else
-      k_route_choose<L, V, B><<<blocks, kThreads, 0, stream>>>(logits, (int)t, (int)e, (int)k, share,
-                                                               ids, weights, workspace);
+      k_route_choose<L, V, B><<<blocks, kChooseThreads, 0, stream>>>(
+          logits, (int)t, (int)e, (int)k, share, ids, weights, workspace);
   };
   auto by_width = [&](auto bf) {
     using Row = std::integral_constant<int, 16>;
@@ -329,9 +344,9 @@ hipError_t launch_route(const void* logits, int bf16, int64_t t, int64_t e, int6
   };
   if (bf16) by_width(std::true_type{});
   else by_width(std::false_type{});
-  if (blocks > 1) {
+  if (t > kOneBlock) {
     int32_t* totals = workspace + (int64_t)blocks * e;
-    if (blocks * e <= kSumMost) {
+    if (sum_wins(blocks, e)) {
       k_route_place<true><<<blocks, kThreads, 0, stream>>>(workspace, nullptr, (int)t, (int)e, (int)k,
                                                            ids, offsets, pairs, slots);
     } else {
