@@ -525,7 +525,8 @@ hipError_t launch_linear_experts(const bl_routing& r, const void* x, int bf16, i
   const bool combine = y_rows == BL_ROWS_TOKENS;
   const int64_t p = r.T * r.k, rows = x_rows == BL_ROWS_TOKENS ? r.T : p;
   const Slots s{r.offsets, r.pairs, (int)r.E, (int)p, x_rows == BL_ROWS_TOKENS ? (int)r.k : 0};
-  if (combine && r.k <= 16 && token_wins(p, r.E) && few_fits(k, (int)r.k, kInt8)) {
+  // the last: blocks of up to 1024 threads, fewer than 2^32 of them in a row of the grid
+  if (combine && r.k <= 16 && token_wins(p, r.E) && few_fits(k, (int)r.k, kInt8) && n < (1 << 25)) {
     auto* f = bf16 ? launch_token<kBf16> : launch_token<kF32>;
     return f(s, r, packed, gamma, x, n, k, y, xq, absmax, stream);
   }

@@ -422,6 +422,25 @@ def test_more_rows_than_a_launch_takes(bl):
     torch.cuda.empty_cache()
 
 
+def test_as_many_outputs_as_there_may_be(bl):
+    """2^26 outputs of one token with 16 experts: more blocks than the kernel of
+    few tokens may launch."""
+    n, k, kk = 1 << 26, 16, 16
+    gen = torch.Generator("cuda").manual_seed(4)
+    packed = torch.full((k, n, kk // 4), 0x55, dtype=torch.uint8, device="cuda")         # t = 0
+    rng = np.random.default_rng(6)
+    tern, small, gam = weights(rng, k, 100, kk)
+    packed[:, :50], packed[:, -50:] = small[:, :50], small[:, 50:]
+    x, _ = activations(1, kk, 7, "f32")
+    r = bl.route_experts(torch.randn(1, k, device="cuda", generator=gen), k)
+    y = bl.linear_experts(x, packed, dev(gam), r, x_rows="tokens")
+    want = bl.linear_experts(x, small, dev(gam), r, x_rows="tokens")
+    assert torch.equal(y[:, :50], want[:, :50]) and torch.equal(y[:, -50:], want[:, 50:])
+    assert int(torch.count_nonzero(y[:, 50:-50])) == 0
+    del packed, y
+    torch.cuda.empty_cache()
+
+
 @pytest.mark.parametrize("t,e,k,kk", [(2, 9, 3, 64), (40, 9, 3, 80), (600, 9, 3, 128), (600, 70, 2, 64)])
 def test_routing_of_anything_stays_in_bounds(bl, t, e, k, kk):
     """Arrays that the router would not write: the calls end and nothing beside
