@@ -137,6 +137,29 @@ def test_route_many_blocks(bl):
     assert np.array_equal(host(r.slots).reshape(-1), slots)
 
 
+def test_route_logits_past_32_bits(bl):
+    """2^22 + 5 tokens of 1024 experts: logits past element 2^32."""
+    t, e = (1 << 22) + 5, 1024
+    x = torch.empty(t, e, dtype=torch.bfloat16, device="cuda")
+    x.normal_(generator=torch.Generator("cuda").manual_seed(1))
+    r = bl.route_experts(x, 2)
+    at = torch.cat([torch.arange(50), torch.arange(t - 50, t), torch.arange(0, t, 99991)]).cuda()
+    some = bits(x[at]).astype(np.uint32) << 16
+    ids, *_ = ref.route(some.view(np.float32), 2)
+    assert np.array_equal(host(r.ids[at]), ids)
+    flat = r.ids.flatten().long()
+    assert int(flat.min()) >= 0 and int(flat.max()) < e
+    count = torch.bincount(flat, minlength=e)
+    assert torch.equal(r.offsets[1:].long(), count.cumsum(0)) and int(r.offsets[0]) == 0
+    # slots and pairs undo each other; along the slots experts, then pairs, grow
+    pairs = r.pairs.long()
+    assert torch.equal(r.slots.flatten().long()[pairs], torch.arange(2 * t, device="cuda"))
+    order = flat[pairs] * (2 * t) + pairs
+    assert bool((order[1:] > order[:-1]).all())
+    del x, r, flat, pairs, order
+    torch.cuda.empty_cache()
+
+
 # ------------------------------------------------------------------ products
 
 def weights(rng, e, n, k):
