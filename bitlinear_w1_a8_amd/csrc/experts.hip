@@ -12,7 +12,6 @@
 namespace bl {
 namespace {
 
-
 // Batches whose step A1 is repeated by every block instead of launched on its
 // own.  Gated, 64 experts of 2560 -> 2 x 1024, 8 per token, on one card: T = 1
 // 7.5 against 9.3 us, T = 2 10.0 / 11.3, T = 4 13.1 / 13.5, T = 6 17.3 / 15.7.
@@ -250,6 +249,8 @@ __global__ __launch_bounds__(512) void k_experts_few(const Slots slots,
 // quantises its slot's row (step A1; every block of the token repeats it) and
 // contracts it with the slot's expert; the teams' exact sums meet in LDS, and
 // the rescale and the sum over the ranks follow in order.  k * team <= 16.
+// Bound by its trips to memory one after another: slot, offsets, row and weights
+// (8 of 64 experts of 1024 -> 2560, 5.2 MB of weights: 5.7 us).
 template <int MODE, int U, int Q>
 __global__ __launch_bounds__(1024) void k_experts_token(const Slots slots,
                                                         const int32_t* __restrict__ slot_of,
@@ -378,7 +379,10 @@ __global__ __launch_bounds__(1024) void k_experts_token(const Slots slots,
   }
 }
 
-// y[t] = sum over j of weights[t, j] * rows[slots[t, j]], in order of j.
+// y[t] = sum over j of weights[t, j] * rows[slots[t, j]], in order of j.  Bound
+// by reading the slots' rows, which the product has just written (2048 tokens
+// of 8 x 2560: 168 MB in, 21 out in 27 us, 7 TB/s, so mostly from the cache
+// behind the L2s).
 __global__ __launch_bounds__(256) void k_experts_combine(const float* __restrict__ rows,
                                                          const int32_t* __restrict__ slots,
                                                          const float* __restrict__ weights, int k,
