@@ -391,11 +391,10 @@ __global__ __launch_bounds__(512) void k_w4_few(const uint4* __restrict__ packed
 // A group's sums are converted and scaled in registers, two VALU operations of
 // four cycles per register and group, against 32 cycles of MFMA per 32 k and
 // fragment: for groups of 32 and 64 that, not the matrix cores, bounds the
-// kernel (2560 -> 6912, 2048 tokens, groups of 64, 71 us: 101 of 163 thousand
-// cycles VALU, 35 MFMA).  So the products of one fragment and group are issued ahead of the
-// scaling of the one before.  Zero points come off the codes (t - z fits
-// an int8; five more operations per word, which all row fragments share) and
-// not off the sums (two operations per register).
+// kernel (2560 -> 6912, 2048 tokens, groups of 64, 69-71 us: 101 of 163 thousand
+// cycles VALU, 35 MFMA).  Zero points come off the codes (t - z fits an int8;
+// five more operations per word, which all row fragments share) and not off the
+// sums (two operations per register).
 //
 // WK > 1 (few tiles): WK groups of waves split K, each with its own stages,
 // and add their sums through LDS in order.
