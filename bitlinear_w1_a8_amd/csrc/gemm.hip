@@ -629,58 +629,88 @@ __global__ __launch_bounds__(WAVES * 64) void k_gemm_lds(const uint32_t* __restr
     lds_sync();
   }
 
+  // The lane's first output: register v of fragment (i, j) is row 32 i + 8 (v / 4)
+  // + v % 4 and column 32 j from it.  Offsets within the tile are the same in
+  // every lane (scalar), and whole tiles need no bounds: with both the
+  // epilogue takes a third of the vector instructions of one that works out each
+  // output's address and bounds.
+  const int row0 = wm * 32 * WMF + h * 4, col0 = n0 + wn * 32 * WNF + m;
+  const bool whole = m0 + BM <= mend && n0 + BN <= N;
+  if constexpr (!SPLIT) {
+    if (acc_out) {
+#pragma unroll
+      for (int i = 0; i < WMF; ++i)
+#pragma unroll
+        for (int v = 0; v < 16; ++v) {
+          const int r = row0 + i * 32 + (v >> 2) * 8 + (v & 3);
+          if (m0 + r >= mend) continue;
+#pragma unroll
+          for (int j = 0; j < WNF; ++j)
+            if (col0 + j * 32 < N)
+              acc_out[(int64_t)(m0 + r) * N + col0 + j * 32] =
+                  exact_sum<WBITS>(acc[i][j][v], rsum[r]);
+        }
+    }
+  }
   if constexpr (GATED) {
+    // Two neighbouring lanes hold a pair's gate and up; of two rows the even
+    // lane takes the first and the odd lane the second, so that every lane
+    // works on an output.
+    const int odd = m & 1;
     const int half = N >> 1;
+    uint16_t* const out = h_out + ((int64_t)(m0 + row0 + odd) * half + (col0 >> 1));
+    auto finish = [&](auto whole_c) {
+      constexpr bool WHOLE = decltype(whole_c)::value;
+#pragma unroll
+      for (int i = 0; i < WMF; ++i) {
+#pragma unroll
+        for (int v = 0; v < 16; v += 2) {
+          const int at = i * 32 + (v >> 2) * 8 + (v & 3), r = row0 + at;
+          const double gg = gm_gate[r + odd], gu = gm_up[r + odd];
+          const int qs0 = rsum[r], qs1 = rsum[r + 1];
+          uint16_t* const o = out + (int64_t)at * half;
+#pragma unroll
+          for (int j = 0; j < WNF; ++j) {
+            const int s0 = exact_sum<WBITS>(acc[i][j][v], qs0);
+            const int s1 = exact_sum<WBITS>(acc[i][j][v + 1], qs1);
+            // every lane takes part: lane l gets what lane l ^ 1 gives
+            const int other = __builtin_amdgcn_update_dpp(0, odd ? s0 : s1, 0xB1, 0xF, 0xF, false);
+            if (WHOLE || (m0 + r + odd < mend && col0 + j * 32 < N))
+              o[j * 16] = gated_relu2_bf16(odd ? other : s0, odd ? s1 : other, gg, gu);
+          }
+        }
+      }
+    };
+    if (whole) finish(std::true_type{});
+    else finish(std::false_type{});
+    return;
+  }
+  float* const out = y + ((int64_t)(m0 + row0) * N + col0);
+  auto finish = [&](auto whole_c) {
+    constexpr bool WHOLE = decltype(whole_c)::value;
 #pragma unroll
     for (int i = 0; i < WMF; ++i) {
 #pragma unroll
       for (int v = 0; v < 16; ++v) {
-        const int r = wm * 32 * WMF + i * 32 + (v >> 2) * 8 + h * 4 + (v & 3);
-        const int tok = m0 + r;
-        const double gg = gm_gate[r], gu = gm_up[r];
+        const int at = i * 32 + (v >> 2) * 8 + (v & 3), r = row0 + at;
+        if (!WHOLE && m0 + r >= mend) continue;
+        const float sc = scale[r];
         const int qs = rsum[r];
+        float* const o = out + (int64_t)at * N;
 #pragma unroll
         for (int j = 0; j < WNF; ++j) {
-          const int n = n0 + wn * 32 * WNF + j * 32 + m;
+          if (!WHOLE && col0 + j * 32 >= N) continue;
           const int sv = exact_sum<WBITS>(acc[i][j][v], qs);
-          // every lane takes part: lane l gets lane l ^ 1's sum
-          const int other = __builtin_amdgcn_update_dpp(0, sv, 0xB1, 0xF, 0xF, false);
-          if (tok >= mend || n >= N) continue;
-          const int64_t o = (int64_t)tok * N + n;
-          if (acc_out) acc_out[o] = sv;
-          if ((m & 1) == 0)
-            h_out[(int64_t)tok * half + (n >> 1)] = gated_relu2_bf16(sv, other, gg, gu);
-        }
-      }
-    }
-    return;
-  }
-#pragma unroll
-  for (int i = 0; i < WMF; ++i) {
-#pragma unroll
-    for (int v = 0; v < 16; ++v) {
-      const int r = wm * 32 * WMF + i * 32 + (v >> 2) * 8 + h * 4 + (v & 3);
-      const int tok = m0 + r;
-      if (tok >= mend) continue;
-      const float sc = scale[r];
-      const int qs = rsum[r];
-#pragma unroll
-      for (int j = 0; j < WNF; ++j) {
-        const int n = n0 + wn * 32 * WNF + j * 32 + m;
-        if (n >= N) continue;
-        const int64_t o = (int64_t)tok * N + n;
-        const int sv = exact_sum<WBITS>(acc[i][j][v], qs);
-        if constexpr (SPLIT) {
           // K split: exact int32 partial sums meet in y (zeroed beforehand,
           // read as int32 until the finishing pass rescales it in place)
-          atomicAdd(reinterpret_cast<int*>(y) + o, sv);
-        } else {
-          if (acc_out) acc_out[o] = sv;
-          y[o] = (float)sv * sc;
+          if constexpr (SPLIT) atomicAdd(reinterpret_cast<int*>(o + j * 32), sv);
+          else o[j * 32] = (float)sv * sc;
         }
       }
     }
-  }
+  };
+  if (whole) finish(std::true_type{});
+  else finish(std::false_type{});
 }
 
 // K split, around the kernel above: y is cleared, receives the exact int32
