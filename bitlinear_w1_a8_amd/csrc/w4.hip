@@ -573,14 +573,22 @@ __global__ __launch_bounds__(WN * WK * 64, WMF == 2 ? 3 : 1) void k_w4_tile(cons
       for (int v = 0; v < 16; ++v)
         for (int k = 0; k < WK - 1; ++k) sum[i][v] += red[k * WN + wn][i * 16 + v][lane];
   }
-  const int col = n0 + wn * 32 + m;
+  // the lane's first output; the others' offsets from it are the same in every
+  // lane (scalar), and whole tiles need no bounds
+  const int col = n0 + wn * 32 + m, row0 = 4 * h;
+  float* const out = y + ((int64_t)(m0 + row0) * N + col);
+  auto finish = [&](auto whole) {
+    constexpr bool WHOLE = decltype(whole)::value;
 #pragma unroll
-  for (int i = 0; i < WMF; ++i)
+    for (int i = 0; i < WMF; ++i)
 #pragma unroll
-    for (int v = 0; v < 16; ++v) {
-      const int row = i * 32 + (v >> 2) * 8 + h * 4 + (v & 3);
-      if (m0 + row < T && col < N) y[(int64_t)(m0 + row) * N + col] = sum[i][v] * scale[row];
-    }
+      for (int v = 0; v < 16; ++v) {
+        const int at = i * 32 + (v >> 2) * 8 + (v & 3);
+        if (WHOLE || (m0 + row0 + at < T && col < N)) out[(int64_t)at * N] = sum[i][v] * scale[row0 + at];
+      }
+  };
+  if (m0 + BM <= T && n0 + BN <= N) finish(std::true_type{});
+  else finish(std::false_type{});
 }
 
 unsigned stream_grid(int64_t units) {
