@@ -23,11 +23,16 @@ constexpr int kFewTokens = 4;
 // 17.5 / 15.9).
 bool token_wins(int64_t p, int64_t e) { return p <= 32 || p <= e; }
 // Slots per expert, were all alike, up to which the experts' rows go to
-// k_experts_few rather than to the tiled kernel (gated, 64 experts of 2560 -> 2
-// x 1024: 8 slots 24.3 against 26.3 us, 16 slots 30.4 / 31.6; 8 experts of 2560
-// -> 2 x 1728: 16 slots 14.6 / 17.2, 32 slots 17.6 / 18.7; 1024 -> 2560: 8
-// slots 18.0 / 18.2, 16 slots 23.7 / 19.8).
-bool few_wins(int64_t p, int64_t e) { return p <= 12 * e; }
+// k_experts_few rather than to the tiled kernel: fewer where that one's tiles
+// fill the device (gated, 64 experts of 2560 -> 2 x 1024: 4 / 6 / 8 slots 22.7 /
+// 23.8 / 26.0 against 24.2 / 24.4 / 25.6 us; 1024 -> 2560: 17.9 / 19.2 at 6 / 8
+// slots against 17.7 / 18.4) than where they do not (8 experts of 2560 -> 2 x
+// 1728: 12 / 24 slots 13.5 / 18.3 against 16.0 / 16.9; 16 experts: 8 / 12 slots
+// 16.8 / 20.3 against 17.5 / 19.1, of 1728 -> 2560 13.0 / 14.1 against 14.9 / 15.1).
+bool few_wins(int64_t p, int64_t e, int64_t n) {
+  const bool fill = std::min(p, e) * ((n + 127) / 128) > 2 * device_cus();
+  return p <= (fill ? 6 : 12) * e;
+}
 
 enum Mode { kInt8 = 0, kBf16 = 1, kF32 = 2 };
 
@@ -496,7 +501,7 @@ hipError_t launch_products(const Slots& s, int64_t x_rows, const uint8_t* packed
   const bool tiled = k >= 64 && x_rows * k < (int64_t(1) << 31) &&
                      n * (k / 16) < (int64_t(1) << 31) &&
                      (n + 127) / 128 * row_blocks(s.P, s.E, 32) < (int64_t(1) << 24) - 8;
-  if (tiled && !few_wins(s.P, s.E))
+  if (tiled && !few_wins(s.P, s.E, n))
     return launch_gemm_experts(s, packed, gamma, gamma2, xq, absmax, n, k, y, h, acc, stream);
   int rows = 16;                       // as many as LDS holds; one of the longest fits
   while (!few_fits(k, rows, kInt8)) rows /= 2;

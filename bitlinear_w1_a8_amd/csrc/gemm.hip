@@ -1022,17 +1022,18 @@ hipError_t run_experts(const Slots& s, const uint8_t* packed, const float* gamma
 
 // Tiles by the slots per expert, were all alike (row blocks are cut per
 // expert, so taller tiles leave more rows empty).  Gated, 64 experts of 2560 ->
-// 2 x 1024, 32 / 64 / 128 / 256 slots each: 64 x 256 tiles 43.3 / 61.0 / 86.3
-// / 128.0 us, 32 x 256 41.0 / 60.1 / 90.5 / 145.1, 32 x 128 41.7 / 64.8 /
-// 101.9 / 169.7 (128-row tiles at 256 slots: 145-158).  Narrow tiles
-// where the wide ones would not give each CU a few blocks (8 experts of 2560 ->
-// 2 x 1728, 16 / 32 slots each: 32 x 128 17.2 / 18.6 us, 32 x 256 18.7 / 19.4).
+// 2 x 1024, 32 / 48 / 64 / 128 / 256 slots each: 64 x 256 tiles 39.7 / 43.3 / 55.9 /
+// 78.7 / 123.7 us, 32 x 256 40.3 / 51.5 / 59.9 / 92.3 / 151.5, 32 x 128 41.8 / 55.7 /
+// 64.4 / 104.7 / 172.8; 1024 -> 2560, 32 / 48 / 64 slots each: 24.9 / 31.0 / 38.3,
+// 23.8 / 29.5 / 39.0, 27.5 / 33.1 / 46.2.  Narrow tiles where the wide
+// ones would not give each CU a few blocks (8 experts of 2560 -> 2 x 1728, 12 / 16 / 24
+// slots each: 32 x 128 16.0 / 16.2 / 17.2 us, 32 x 256 16.6 / 16.6 / 16.9).
 template <bool GATED>
 hipError_t tile_experts(const Slots& s, const uint8_t* packed, const float* gamma,
                         const float* gamma2, const int8_t* xq, const float* absmax, int64_t n,
                         int64_t k, float* y, uint16_t* h, int32_t* acc, hipStream_t stream) {
   const int64_t each = s.P / std::min(s.P, s.E), hit = std::min(s.P, s.E);
-  if (each >= 96)
+  if (each >= 48)
     return run_experts<4, 1, 2, 2, 3, GATED>(s, packed, gamma, gamma2, xq, absmax, n, k, y, h, acc,
                                              stream);
   if (hit * ((each + 31) / 32) * ((n + 255) / 256) >= 2 * device_cus())

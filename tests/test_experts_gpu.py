@@ -201,7 +201,8 @@ GATED = [(1, 8, 2, 40, 256, "bf16", "normal"), (1, 64, 8, 1024, 2560, "bf16", "n
          (40, 4, 2, 33, 16400, "bf16", "normal"), (3, 3, 2, 9, 131072, "bf16", "normal"),
          (20, 2, 1, 17, 40000, "f32", "normal"), (400, 3, 2, 70, 272, "bf16", "masked"),
          (2, 4, 2, 20, 8208, "f32", "normal"), (50, 200, 3, 40, 256, "bf16", "masked"),
-         (300, 1000, 4, 24, 128, "bf16", "ties"), (4, 1024, 8, 16, 80, "f32", "normal")]
+         (300, 1000, 4, 24, 128, "bf16", "ties"), (4, 1024, 8, 16, 80, "f32", "normal"),
+         (600, 520, 8, 20, 208, "bf16", "normal"), (600, 520, 8, 24, 256, "bf16", "masked")]
 
 
 @pytest.mark.parametrize("t,e,k,n,kk,dtype,kind", GATED,
@@ -242,7 +243,8 @@ LINEAR = [(1, 8, 2, 40, 256, "bf16", "normal"), (1, 64, 8, 2560, 1024, "bf16", "
           (40, 4, 2, 33, 16400, "bf16", "normal"), (2, 3, 1, 9, 131072, "bf16", "normal"),
           (1, 4, 4, 18, 36880, "f32", "normal"), (400, 3, 2, 70, 272, "bf16", "masked"),
           (50, 200, 3, 40, 256, "bf16", "masked"), (300, 1000, 4, 24, 128, "bf16", "ties"),
-          (4, 1024, 8, 17, 80, "f32", "normal"), (6, 64, 17, 30, 96, "bf16", "normal")]
+          (4, 1024, 8, 17, 80, "f32", "normal"), (6, 64, 17, 30, 96, "bf16", "normal"),
+          (600, 520, 8, 24, 208, "bf16", "masked"), (600, 520, 8, 20, 256, "bf16", "normal")]
 
 
 @pytest.mark.parametrize("x_rows", ["slots", "tokens"])
