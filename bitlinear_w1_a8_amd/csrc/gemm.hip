@@ -631,9 +631,10 @@ __global__ __launch_bounds__(WAVES * 64) void k_gemm_lds(const uint32_t* __restr
 
   // The lane's first output: register v of fragment (i, j) is row 32 i + 8 (v / 4)
   // + v % 4 and column 32 j from it.  Offsets within the tile are the same in
-  // every lane (scalar), and whole tiles need no bounds: with both the
-  // epilogue takes a third of the vector instructions of one that works out each
-  // output's address and bounds.
+  // every lane (scalar), and whole tiles need no bounds.  Against an epilogue that
+  // works out each output's address and bounds: T = 2048, 2560 -> 6912 43.0 -> 39.8
+  // us; routed, 16384 slots of 1024 -> 2560 97 -> 90 us, VALU issue 71 -> 59
+  // thousand cycles.
   const int row0 = wm * 32 * WMF + h * 4, col0 = n0 + wn * 32 * WNF + m;
   const bool whole = m0 + BM <= mend && n0 + BN <= N;
   if constexpr (!SPLIT) {
@@ -655,7 +656,7 @@ __global__ __launch_bounds__(WAVES * 64) void k_gemm_lds(const uint32_t* __restr
   if constexpr (GATED) {
     // Two neighbouring lanes hold a pair's gate and up; of two rows the even
     // lane takes the first and the odd lane the second, so that every lane
-    // works on an output.
+    // works on an output (T = 2048, 2560 -> 2 x 6912: 95.6 -> 78.2 us).
     const int odd = m & 1;
     const int half = N >> 1;
     uint16_t* const out = h_out + ((int64_t)(m0 + row0 + odd) * half + (col0 >> 1));

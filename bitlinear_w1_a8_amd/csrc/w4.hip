@@ -391,7 +391,7 @@ __global__ __launch_bounds__(512) void k_w4_few(const uint4* __restrict__ packed
 // A group's sums are converted and scaled in registers, two VALU operations of
 // four cycles per register and group, against 32 cycles of MFMA per 32 k and
 // fragment: for groups of 32 and 64 that, not the matrix cores, bounds the
-// kernel (2560 -> 6912, 2048 tokens, groups of 64, 69-71 us: 101 of 163 thousand
+// kernel (2560 -> 6912, 2048 tokens, groups of 64, 69-71 us: 98 of 159 thousand
 // cycles VALU, 35 MFMA).  Zero points come off the codes (t - z fits an int8;
 // five more operations per word, which all row fragments share) and not off the
 // sums (two operations per register).
