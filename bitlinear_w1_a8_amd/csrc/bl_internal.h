@@ -173,6 +173,15 @@ __device__ __forceinline__ void lds_sync() {
   __asm__ volatile("" ::: "memory");
 }
 
+// Between LDS writes of some lanes of a wave and reads of them by others of the
+// same wave.  The hardware keeps a wave's LDS operations in order; the fence
+// has the compiler keep them so too (it makes no instruction).
+__device__ __forceinline__ void wave_lds_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 // Wait until at most N vector-memory operations of this wave are outstanding.
 template <int N>
 __device__ __forceinline__ void wait_vmem() {

@@ -351,9 +351,10 @@ __global__ __launch_bounds__(1024) void k_experts_token(const Slots slots,
     }
     if (out && part == 0 && lane == 0) absmax_out[row] = a;
     sum = wave_sum_i(sum);
+    wave_lds_sync();                                  // this wave's own chunks: no block barrier
     // every column of the second operand is the one row: each holds the sums
     v4i acc = {0, 0, 0, 0};
-    const unsigned char* xq = xs + j * stride + 64 * qg;   // this wave's own chunks: no barrier
+    const unsigned char* xq = xs + j * stride + 64 * qg;
     for (int b0 = c0; b0 < c1; b0 += U) {
 #pragma unroll
       for (int u = 0; u < U; ++u) {
