@@ -595,16 +595,15 @@ unsigned stream_grid(int64_t units) {
   return (unsigned)std::min<int64_t>((units + 255) / 256, 16 * (int64_t)device_cus());
 }
 
+// f(G, ZEROS), which launches and returns the launch's status.
 template <typename F>
 hipError_t by_group(int g, bool zeros, F&& f) {
-  auto z = [&](auto gc) {
-    if (zeros) f(gc, std::true_type{});
-    else f(gc, std::false_type{});
+  auto z = [&](auto gc) -> hipError_t {
+    return zeros ? f(gc, std::true_type{}) : f(gc, std::false_type{});
   };
-  if (g == 32) z(std::integral_constant<int, 32>{});
-  else if (g == 64) z(std::integral_constant<int, 64>{});
-  else z(std::integral_constant<int, 128>{});
-  return hipGetLastError();
+  if (g == 32) return z(std::integral_constant<int, 32>{});
+  if (g == 64) return z(std::integral_constant<int, 64>{});
+  return z(std::integral_constant<int, 128>{});
 }
 
 }  // namespace
@@ -619,8 +618,9 @@ hipError_t launch_pack_w4(const float* w, int64_t n, int64_t k, int g, uint8_t* 
       using I = decltype(ic);
       k_pack_w4<decltype(gc)::value, decltype(zc)::value, I><<<grid, 256, 0, stream>>>(
           w, (I)units, (int)k, reinterpret_cast<uint4*>(packed), scales, zeros);
+      return hipGetLastError();
     };
-    small ? go(uint32_t{}) : go(uint64_t{});
+    return small ? go(uint32_t{}) : go(uint64_t{});
   });
 }
 
@@ -659,6 +659,7 @@ hipError_t launch_forward_w4(const uint8_t* packed, const uint16_t* scales, cons
           if (k % kBlock) kern = k_w4_tile<WN, WK, WMF, G, Z, true>;
         kern<<<(unsigned)((tiles(32 * WMF, 32 * WN) + 7) / 8 * 8), 64 * WN * WK, 0, stream>>>(
             w, scales, zeros, xq, absmax, (int)t, (int)n, (int)k, y);
+        return hipGetLastError();
       };
       using I1 = std::integral_constant<int, 1>;
       using I2 = std::integral_constant<int, 2>;
@@ -692,19 +693,18 @@ hipError_t launch_forward_w4(const uint8_t* packed, const uint16_t* scales, cons
     // (2560 -> 128256, one token: 1 / 2 / 3 / 4 blocks 43 / 33 / 35 / 34 us)
     const int64_t per_cu = lds + 12288 <= (size_t)kMaxLds / 2 ? 2 : 1;
     const int64_t grid = std::min<int64_t>((tiles * team + 7) / 8, per_cu * device_cus());
-    hipError_t e = hipSuccess;
-    by_group(g, zeros != nullptr, [&](auto gc, auto zc) {
+    const hipError_t e = by_group(g, zeros != nullptr, [&](auto gc, auto zc) {
       constexpr int G = decltype(gc)::value;
       constexpr bool Z = decltype(zc)::value;
       auto go = [&](auto kern) {
-        e = kern.allow_lds();
-        if (e != hipSuccess) return;
+        const hipError_t lds_ok = kern.allow_lds();
+        if (lds_ok != hipSuccess) return lds_ok;
         kern.kernel<<<(unsigned)grid, 512, lds, stream>>>(w, scales, zeros, xq + t0 * k, absmax + t0,
                                                    (int)nt, (int)n, (int)k, team, y + t0 * n);
-        e = hipGetLastError();
+        return hipGetLastError();
       };
-      if (nt == 1) go(Kernel<k_w4_few<G, Z, 1, kAhead>>{});
-      else go(Kernel<k_w4_few<G, Z, 4, kAhead>>{});
+      return nt == 1 ? go(Kernel<k_w4_few<G, Z, 1, kAhead>>{})
+                     : go(Kernel<k_w4_few<G, Z, 4, kAhead>>{});
     });
     if (e != hipSuccess) return e;
   }
