@@ -6,10 +6,9 @@
 #include "bitlinear_experts.h"
 #include "bitlinear_w4.h"
 #include "bl_internal.h"
+#include "w4_plan.h"
 
 namespace bl {
-
-constexpr int kMaxLds = 150 * 1024;   // dynamic LDS of a block (a CU has 160 KiB, the static part included)
 
 // A kernel that may ask for more dynamic LDS than the 64 KiB that a launch
 // gets without saying so; said once per kernel and device (saying it again,

@@ -20,7 +20,6 @@
 namespace bl {
 namespace {
 
-constexpr int kBlock = 128;      // weights per packed block (64 bytes)
 typedef float v16f __attribute__((ext_vector_type(16)));
 
 __device__ __forceinline__ float bf16_f(uint16_t b) { return __uint_as_float((uint32_t)b << 16); }
@@ -184,17 +183,8 @@ struct Run {
   }
 };
 
-// Blocks of 128 k that a wave of k_w4_few loads at a time, into each of two
-// buffers (2560 -> 128256, one token: 2 / 4 / 5 / 8 blocks 34.7 / 34.5 / 35.0
-// / 40.0 us; 8192 -> 28672: 34.6 / 28.9 / 34.4 / 31.4).
-constexpr int kAhead = 4;
-
-// LDS row stride of a token: whole blocks of 128 k, and 16 bytes that spread
-// the rows of one operand read over the banks.
-__host__ __device__ constexpr int token_stride(int k) { return ((k + 127) & ~127) + 16; }
-
-// Up to 16 tokens (decode): the weights stream once.  The tokens' int8 rows are
-// whole in LDS.  A team of `team` waves has 16 weight rows and splits their
+// A few tokens (decode), as many as LDS holds whole (16 of rows up to 9472, one
+// of the longest): the weights stream once.  A team of `team` waves has 16 weight rows and splits their
 // blocks into runs; a wave holds two buffers of U blocks (1 KiB each), one on
 // its way while it works on the other, and goes on to its next rows without a
 // pause where it is a team of its own.  Bound by the weight stream (2560 ->
@@ -213,7 +203,7 @@ __global__ __launch_bounds__(512) void k_w4_few(const uint4* __restrict__ packed
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int q = lane >> 4, r = lane & 15;
-  const int blocks = (K + kBlock - 1) / kBlock, kg = K / G, stride = token_stride(K);
+  const int blocks = (K + kBlock - 1) / kBlock, kg = K / G, stride = (int)token_stride(K);
   const int tiles = (N + 15) / 16, teams = 8 / team;
   const int part = wave % team;
   const int per = (blocks + team - 1) / team;       // blocks of a wave's run
@@ -644,20 +634,19 @@ hipError_t launch_forward_w4(const uint8_t* packed, const uint16_t* scales, cons
                              const int8_t* xq, const float* absmax, int64_t t, int64_t n,
                              int64_t k, int g, float* y, hipStream_t stream) {
   const auto* w = reinterpret_cast<const uint4*>(packed);
-  if (t > 16) {
-    const int64_t cus = device_cus();
-    auto tiles = [&](int64_t rows, int64_t cols) {
-      return ((t + rows - 1) / rows) * ((n + cols - 1) / cols);
-    };
+  const W4Plan plan = w4_plan(t, n, k, g, device_cus());
+  if (plan.wn) {
     return by_group(g, zeros != nullptr, [&](auto gc, auto zc) {
       constexpr int G = decltype(gc)::value;
       constexpr bool Z = decltype(zc)::value;
       auto go = [&](auto wn, auto wk, auto wmf) {
         constexpr int WN = decltype(wn)::value, WK = decltype(wk)::value, WMF = decltype(wmf)::value;
+        constexpr int BM = 32 * WMF, BN = 32 * WN;
         auto kern = k_w4_tile<WN, WK, WMF, G, Z, false>;
         if constexpr (G < kBlock)
           if (k % kBlock) kern = k_w4_tile<WN, WK, WMF, G, Z, true>;
-        kern<<<(unsigned)((tiles(32 * WMF, 32 * WN) + 7) / 8 * 8), 64 * WN * WK, 0, stream>>>(
+        const int64_t tiles = ((t + BM - 1) / BM) * ((n + BN - 1) / BN);
+        kern<<<(unsigned)((tiles + 7) / 8 * 8), 64 * WN * WK, 0, stream>>>(
             w, scales, zeros, xq, absmax, (int)t, (int)n, (int)k, y);
         return hipGetLastError();
       };
@@ -665,29 +654,18 @@ hipError_t launch_forward_w4(const uint8_t* packed, const uint16_t* scales, cons
       using I2 = std::integral_constant<int, 2>;
       using I4 = std::integral_constant<int, 4>;
       using I8 = std::integral_constant<int, 8>;
-      // the smallest tiles, with K split most, that do not outnumber the CUs
-      // (see above)
-      if (tiles(32, 32) <= cus) return go(I1{}, I8{}, I1{});
-      if (tiles(32, 64) <= cus) return go(I2{}, I4{}, I1{});
-      if (tiles(32, 128) <= cus) return go(I4{}, I2{}, I1{});
-      if (G == 128 && 8 * tiles(128, 256) >= 5 * cus) return go(I8{}, I1{}, I4{});
-      if (4 * tiles(64, 128) >= 5 * cus) return go(I4{}, I1{}, I2{});
-      return go(I4{}, I1{}, I1{});
+      if (plan.wn == 1) return go(I1{}, I8{}, I1{});
+      if (plan.wn == 2) return go(I2{}, I4{}, I1{});
+      if constexpr (G == kBlock)
+        if (plan.wn == 8) return go(I8{}, I1{}, I4{});
+      if (plan.wk == 2) return go(I4{}, I2{}, I1{});
+      return plan.wmf == 2 ? go(I4{}, I1{}, I2{}) : go(I4{}, I1{}, I1{});
     });
   }
-  // as many tokens at a time as LDS holds
-  const int64_t stride = token_stride((int)k), most = std::min<int64_t>(16, kMaxLds / stride);
-  const int64_t tiles = (n + 15) / 16, blocks = (k + kBlock - 1) / kBlock;
-  // K split over a team of waves while there are too few tiles to fill the
-  // device and a wave would have more than one load group (2560 -> 2560, one
-  // token: teams of 4 / 8 5.2 / 4.3 us; 2560 -> 16384: 1 / 2 / 4 8.2 / 8.6 / 8.5).
-  // Several tokens are staged by every block, so for them fewer, larger ones
-  // (2560 -> 6912, 7 tokens, groups of 32: teams of 4 / 8 10.1 / 13.5 us).
-  const int64_t want = t == 1 ? 2048 : 1024;
-  int team = 1;
-  while (team < 8 && tiles * team < want && blocks > kAhead * team) team *= 2;
-  for (int64_t t0 = 0; t0 < t; t0 += most) {
-    const int64_t nt = std::min(t - t0, most);
+  const int64_t stride = token_stride(k), tiles = (n + 15) / 16;
+  const int team = plan.team;
+  for (int64_t t0 = 0; t0 < t; t0 += plan.tokens) {
+    const int64_t nt = std::min(t - t0, plan.tokens);
     const size_t lds = (size_t)(nt * stride);
     // two blocks per CU where their LDS fits, going on from tile to tile
     // (2560 -> 128256, one token: 1 / 2 / 3 / 4 blocks 43 / 33 / 35 / 34 us)

@@ -1,0 +1,70 @@
+// Which kernel a 4-bit product takes: plain C++, so that the choice can be
+// asked without a device.
+#pragma once
+
+#include <stdint.h>
+
+#include <algorithm>
+
+namespace bl {
+
+constexpr int kMaxLds = 150 * 1024;   // dynamic LDS of a block (a CU has 160 KiB, the static part included)
+
+constexpr int kBlock = 128;           // weights per packed block (64 bytes)
+
+// Blocks of 128 k that a wave of k_w4_few loads at a time, into each of two
+// buffers (2560 -> 128256, one token: 2 / 4 / 5 / 8 blocks 34.7 / 34.5 / 35.0
+// / 40.0 us; 8192 -> 28672: 34.6 / 28.9 / 34.4 / 31.4).
+constexpr int kAhead = 4;
+
+// LDS row stride of a token of k_w4_few: whole blocks of 128 k, and 16 bytes
+// that spread the rows of one operand read over the banks.
+constexpr int64_t token_stride(int64_t k) { return (k + kBlock - 1) / kBlock * kBlock + 16; }
+
+struct W4Plan {
+  // k_w4_tile<wn, wk, wmf>, or with wn = 0 k_w4_few
+  int wn, wk, wmf;
+  // k_w4_few: waves that split K, and tokens per pass over the matrix
+  int team;
+  int64_t tokens;
+};
+
+// T tokens, N rows of K weights in groups of G, on `cus` compute units.
+inline W4Plan w4_plan(int64_t t, int64_t n, int64_t k, int g, int64_t cus) {
+  auto tiles = [&](int64_t rows, int64_t cols) {
+    return ((t + rows - 1) / rows) * ((n + cols - 1) / cols);
+  };
+  // k_w4_few keeps whole tokens in LDS: as many at a time as it holds, and a
+  // pass over the matrix for each lot.  k_w4_tile reads the matrix once, so it
+  // has the batches that would take three passes or more, and those of two but
+  // for matrices so small that their tiles leave CUs idle and K is cut over
+  // eight waves.  us, k_w4_few / k_w4_tile, 28672 -> 8192: 6 tokens (2 passes)
+  // 92.7 / 41.4, 16 (4) 174.6 / 43.0; 14336 -> 8192: 12 (2) 52.7 / 22.9; 28672 ->
+  // 4096: 6 (2) 51.0 / 36.7; 28672 -> 2560: 6 (2) 33.3 / 37.9, 10 (2) 36.9 / 39.0, 12
+  // (3) 52.2 / 39.6; 14336 -> 2560: 11 (2) 22.4 / 24.1, groups of 32 16 (2) 27.4 / 23.1;
+  // 28672 -> 1024: 10 (2) 32.3 / 35.9, 11 (3) 43.2 / 36.3; 131072 -> 1024: 2 (2) 106.8 /
+  // 145.2, 4 (4) 199.9 / 146.2; 10240 -> 128256: 16 (2) 307 / 248.
+  const int64_t most = std::min<int64_t>(16, kMaxLds / token_stride(k));
+  const int64_t passes = (t + most - 1) / most, tiles16 = (n + 15) / 16;
+  if (t <= 16 && (passes == 1 || (passes == 2 && tiles16 < cus))) {
+    // K split over a team of waves while there are too few tiles to fill the
+    // device and a wave would have more than one load group (2560 -> 2560, one
+    // token: teams of 4 / 8 5.2 / 4.3 us; 2560 -> 16384: 1 / 2 / 4 8.2 / 8.6 / 8.5).
+    // Several tokens are staged by every block, so for them fewer, larger ones
+    // (2560 -> 6912, 7 tokens, groups of 32: teams of 4 / 8 10.1 / 13.5 us).
+    const int64_t want = t == 1 ? 2048 : 1024, blocks = (k + kBlock - 1) / kBlock;
+    int team = 1;
+    while (team < 8 && tiles16 * team < want && blocks > kAhead * team) team *= 2;
+    return {0, 0, 0, team, most};
+  }
+  // the smallest tiles, with K split most, that do not outnumber the CUs; then
+  // larger ones while each CU still gets one or more
+  if (tiles(32, 32) <= cus) return {1, 8, 1, 0, 0};
+  if (tiles(32, 64) <= cus) return {2, 4, 1, 0, 0};
+  if (tiles(32, 128) <= cus) return {4, 2, 1, 0, 0};
+  if (g == 128 && 8 * tiles(128, 256) >= 5 * cus) return {8, 1, 4, 0, 0};
+  if (4 * tiles(64, 128) >= 5 * cus) return {4, 1, 2, 0, 0};
+  return {4, 1, 1, 0, 0};
+}
+
+}  // namespace bl
