@@ -1,7 +1,12 @@
 """Which kernel a 4-bit product takes, asked on the host."""
 
+import numpy as np
 import pytest
+import torch
 
+from bitlinear_w1_a8_amd import workloads as wl
+from oracle import w4_ref as ref
+from tests import w4_cases
 from tests.w4_plan import compiled
 
 CUS = 256
@@ -43,3 +48,52 @@ def test_team_splits_no_further_than_load_groups(plan):
             for k in (128, 512, 640, 1024, 2560, 8192):
                 team = plan(t, n, k, 128, CUS).team
                 assert team in (1, 2, 4, 8) and (team == 1 or 4 * (team // 2) < -(-k // 128))
+
+
+def test_cases_reach_every_variant(plan):
+    """Every kernel that the rule can choose has a case in w4_cases, with all
+    group sizes, whole and partial tiles, whole and half last blocks, and every
+    remainder of the three stages."""
+    for (wn, wk, wmf), shapes in w4_cases.TILED.items():
+        groups, stages = set(), set()
+        for t, n, gk in shapes:
+            assert t > 32 * wmf and t % (32 * wmf) and n > 32 * wn and n % (32 * wn)
+            for g, k in gk:
+                assert plan(t, n, k, g, CUS)[:3] == (wn, wk, wmf)
+                groups.add((g, k % 128 != 0))
+                stages.add(-(-(-(-k // 128)) // wk) % 3)
+        whole = {(128, False)} if wmf == 4 else {(32, False), (64, False), (128, False), (32, True), (64, True)}
+        assert groups >= whole, (wn, groups)
+        assert stages == {0, 1, 2}, (wn, wk, wmf, stages)
+    few = {(t > 1, g, plan(t, n, k, g, CUS).team) for t, n, k, g in w4_cases.FEW}
+    assert all(plan(t, n, k, g, CUS).wn == 0 for t, n, k, g in w4_cases.FEW)
+    assert few >= {(many, g, team) for many in (False, True) for g in (32, 64, 128) for team in (1, 2, 4, 8)}
+    for t, n, k, g in w4_cases.PASSES:
+        assert passes(plan(t, n, k, g, CUS), t) == 2
+    assert any(t % plan(t, n, k, g, CUS).tokens == 1 for t, n, k, g in w4_cases.PASSES)
+    assert {plan(t, n, k, g, CUS)[:3] for t, n, k, g in w4_cases.LONG} == {(1, 8, 1), (2, 4, 1)}
+
+
+def test_variants_are_all_that_the_rule_gives(plan):
+    """The rule over a grid of sizes gives no variant that has no case."""
+    seen = {plan(t, n, k, g, CUS)[:3] for t in (1, 2, 9, 16, 17, 40, 64, 100, 300, 700, 2048, 9000)
+            for n in (1, 33, 500, 2560, 4096, 6912, 30000, 128256) for k in (128, 2560, 8192, 28672, 131072)
+            for g in (32, 64, 128)}
+    assert seen == set(w4_cases.TILED) | {(0, 0, 0)}
+
+
+@pytest.mark.parametrize("with_zeros", [False, True])
+@pytest.mark.parametrize("t,n,k,g", [(3, 9, 416, 32), (1, 5, 320, 64), (4, 7, 256, 128)])
+def test_reference_is_the_oracles(t, n, k, g, with_zeros):
+    rng = np.random.default_rng(k)
+    codes = rng.integers(-8, 8, (n, k)).astype(np.int8)
+    s = wl.bf16_bits(rng.uniform(0.002, 0.02, (n, k // g)).astype(np.float32))
+    z = rng.integers(-8, 8, (n, k // g)).astype(np.int8) if with_zeros else np.zeros((n, k // g), np.int8)
+    q = rng.integers(-127, 128, (t, k)).astype(np.int8)
+    a = rng.uniform(0, 4, t).astype(np.float32)
+    a[0] = 0.0
+    want, size = ref.forward(codes, s, z, q, a)
+    got, gsize = w4_cases.forward(torch.from_numpy(ref.pack(codes)),
+                                  torch.from_numpy(s.view(np.int16)).view(torch.bfloat16),
+                                  torch.from_numpy(z) if with_zeros else None, torch.from_numpy(q), torch.from_numpy(a))
+    assert np.allclose(got.numpy(), want, rtol=1e-14, atol=0) and np.allclose(gsize.numpy(), size, rtol=1e-14, atol=0)
