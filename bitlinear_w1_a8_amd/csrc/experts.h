@@ -6,6 +6,7 @@
 #include "bitlinear_experts.h"
 #include "bitlinear_w4.h"
 #include "bl_internal.h"
+#include "experts_plan.h"
 #include "w4_plan.h"
 
 namespace bl {

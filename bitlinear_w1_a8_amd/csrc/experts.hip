@@ -463,12 +463,19 @@ hipError_t launch_few(const Slots& s, const uint8_t* packed, const float* gamma,
     }
     return e;
   };
-  if (k < 64) return go(Kernel<k_experts_few<MODE, GATED, 4, kWords>>{});
-  if (k % 64)
-    return k <= 1024 ? go(Kernel<k_experts_few<MODE, GATED, 4, kShort>>{})
-                     : go(Kernel<k_experts_few<MODE, GATED, 10, kShort>>{});
-  return k <= 1024 ? go(Kernel<k_experts_few<MODE, GATED, 4, kWhole>>{})
-                   : go(Kernel<k_experts_few<MODE, GATED, 10, kWhole>>{});
+  if (k < 64) return go(Kernel<k_experts_few<MODE, GATED, 2, kWords>>{});
+  auto by_depth = [&](auto quads) {
+    constexpr int Q = decltype(quads)::value;
+    switch (few_depth(k)) {
+      case 2: return go(Kernel<k_experts_few<MODE, GATED, 2, Q>>{});
+      case 4: return go(Kernel<k_experts_few<MODE, GATED, 4, Q>>{});
+      case 6: return go(Kernel<k_experts_few<MODE, GATED, 6, Q>>{});
+      case 8: return go(Kernel<k_experts_few<MODE, GATED, 8, Q>>{});
+      default: return go(Kernel<k_experts_few<MODE, GATED, 10, Q>>{});
+    }
+  };
+  return k % 64 ? by_depth(std::integral_constant<int, kShort>{})
+                : by_depth(std::integral_constant<int, kWhole>{});
 }
 
 template <int MODE>
