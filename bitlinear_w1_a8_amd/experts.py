@@ -6,6 +6,7 @@ the caller's device and every step runs in the library's HIP kernels on the
 current stream of that device.
 """
 
+import operator
 import struct
 
 import torch
@@ -96,9 +97,9 @@ def route_experts(logits, k, share="chosen"):
         raise ValueError(f"share must be one of {sorted(SHARES)}, got {share!r}")
     t, e = shape = logits.shape
     need(dev, logits, "logits", logits.dtype, shape)
-    k = int(k)
-    if k < 1:
-        raise ValueError(f"k must be at least 1, got {k}")
+    k = operator.index(k)
+    if not 1 <= k <= MAX_TOP_K:              # before anything of that size is allocated
+        raise ValueError(f"k must be in [1, {MAX_TOP_K}], got {k}")
     on, p = logits.device, t * k
     wsb = lib.bitlinear_route_workspace_bytes(t, e)
     weights = torch.empty((t, k), dtype=torch.float32, device=on)
