@@ -2,6 +2,8 @@
 (include/bitlinear_w4.h), same names: packing, unpacking, the product with
 step A1's int8 tokens.  Argument marshalling only, as ``binding``."""
 
+import operator
+
 import torch
 
 from . import binding
@@ -52,7 +54,7 @@ def pack_weights_w4(w, group=128, with_zeros=False):
         raise ValueError("w must be [N, K]")
     n, k = shape = w.shape
     need(dev, w, "w", torch.float32, shape)
-    group, on = int(group), w.device
+    group, on = operator.index(group), w.device
     if group not in (32, 64, 128) or k % group:
         raise ValueError(f"group must be 32, 64 or 128 and divide K={k}, got {group}")
     packed = torch.empty((n, (k + 127) // 128 * 64), dtype=torch.uint8, device=on)
@@ -66,7 +68,7 @@ def pack_weights_w4(w, group=128, with_zeros=False):
 def unpack_weights_w4(packed, scales, zeros, k):
     """The float32 values [N, k] that a packed matrix stands for."""
     lib = _load()
-    k, dev = int(k), device_of(packed, "packed")
+    k, dev = operator.index(k), device_of(packed, "packed")
     n, group = _matrix(dev, packed, scales, zeros, k)
     w = torch.empty((n, k), dtype=torch.float32, device=packed.device)
     call(dev, lib.bitlinear_unpack_weights_w4, packed.data_ptr(), scales.data_ptr(),
