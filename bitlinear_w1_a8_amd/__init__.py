@@ -15,8 +15,9 @@ _W4 = ("pack_weights_w4", "unpack_weights_w4", "forward_w4")
 
 def __getattr__(name):
     if name in _EXPORTS:
-        from . import binding as module
-    elif name in _EXPERTS:
+        from . import binding                         # looked up every time, as it may be replaced there
+        return getattr(binding, name)
+    if name in _EXPERTS:
         from . import experts as module
     elif name in _W4:
         from . import w4 as module
