@@ -47,14 +47,17 @@ inline W4Plan w4_plan(int64_t t, int64_t n, int64_t k, int g, int64_t cus) {
   const int64_t most = std::min<int64_t>(16, kMaxLds / token_stride(k));
   const int64_t passes = (t + most - 1) / most, tiles16 = (n + 15) / 16;
   if (t <= 16 && (passes == 1 || (passes == 2 && tiles16 < cus))) {
-    // K split over a team of waves while there are too few tiles to fill the
-    // device and a wave would have more than one load group (2560 -> 2560, one
-    // token: teams of 4 / 8 5.2 / 4.3 us; 2560 -> 16384: 1 / 2 / 4 8.2 / 8.6 / 8.5).
-    // Several tokens are staged by every block, so for them fewer, larger ones
-    // (2560 -> 6912, 7 tokens, groups of 32: teams of 4 / 8 10.1 / 13.5 us).
-    const int64_t want = t == 1 ? 2048 : 1024, blocks = (k + kBlock - 1) / kBlock;
+    // K split over a team of waves while a wave has more than one load group and
+    // twice the team still leaves one block per CU, two for one token (several
+    // tokens are staged by every block: 2560 -> 6912, 7 tokens, groups of 32, teams
+    // of 4 / 8 10.1 / 13.5 us).  Up to the border itself: 28672 -> 8192, where a team of
+    // 4 makes one block per CU, 5 tokens, teams of 2 / 4 / 8 55.0 / 34.5 / 35.9 us, and
+    // just beyond it, 28672 -> 8320, 55.3 / 56.2 / 47.5; 2560 -> 16384, 8 tokens, 1 / 2 / 4
+    // 12.7 / 9.9 / 9.8; one token, 28672 -> 8192, 4 / 8 33.9 / 27.3, 2560 -> 16384, 2 / 4
+    // 8.9 / 8.5.
+    const int64_t per_cu = t == 1 ? 2 : 1, blocks = (k + kBlock - 1) / kBlock;
     int team = 1;
-    while (team < 8 && tiles16 * team < want && blocks > kAhead * team) team *= 2;
+    while (team < 8 && 2 * tiles16 * team <= 8 * per_cu * cus && blocks > kAhead * team) team *= 2;
     return {0, 0, 0, team, most};
   }
   // the smallest tiles, with K split most, that do not outnumber the CUs; then

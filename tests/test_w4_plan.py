@@ -97,3 +97,15 @@ def test_reference_is_the_oracles(t, n, k, g, with_zeros):
                                   torch.from_numpy(s.view(np.int16)).view(torch.bfloat16),
                                   torch.from_numpy(z) if with_zeros else None, torch.from_numpy(q), torch.from_numpy(a))
     assert np.allclose(got.numpy(), want, rtol=1e-14, atol=0) and np.allclose(gsize.numpy(), size, rtol=1e-14, atol=0)
+
+
+def test_team_fills_the_device(plan):
+    """No team is half as large as it could be with its blocks of eight waves
+    still one per CU (two for one token)."""
+    for t in (1, 2, 5, 16):
+        for n in (16, 2560, 4080, 4096, 4112, 6912, 8192, 8208, 16384, 16400, 32768, 32784):
+            for k in (512, 1280, 2560, 8192, 28672):
+                p = plan(t, n, k, 128, CUS)
+                if p.wn or p.team == 8 or -(-k // 128) <= 4 * p.team:
+                    continue
+                assert -(-n // 16) * 2 * p.team / 8 > (2 if t == 1 else 1) * CUS, (t, n, k, p)
