@@ -97,9 +97,11 @@ __host__ __device__ constexpr int few_stride(int k) { return ((k + 255) & ~255) 
 // q comes off at the end.  No wave waits for another after the rows are staged
 // and none adds to another's sums, so a wave is one run of loads: its first U
 // chunks (256 k of 16 rows, 1 KiB) are in flight while the rows are staged.
-// Bound by the weight stream (gated, 33 tokens, 6 of 64 experts each, 2560 -> 2 x 1000:
-// 79 MB in 14.5 us, 5.4 TB/s; one token, 8 experts, 2560 -> 2 x 1024: 7.1 us, of
-// which the launch and three dependent loads are more than half).
+// Gated, 33 tokens, 6 of 64 experts each, 2560 -> 2 x 1000, weights from memory: the
+// 45 experts hit, 58 MB, in 18.5 us (3.1 TB/s; 15.2 where part of the weights is
+// still in the cache behind the L2s): the waves wait, VALU issue is 17 thousand
+// of some 44 thousand cycles.  One token, 8 experts, 2560 -> 2 x 1024: 8.7 us, of
+// which the launch and three dependent loads are more than half.
 // MODE kBf16, kF32: step A1 happens in the staging (every block of an expert
 // repeats it: for batches of a few tokens, whose own launch would cost more),
 // and the first block of an expert writes the codes and absmax of the tokens
@@ -255,7 +257,8 @@ __global__ __launch_bounds__(512) void k_experts_few(const Slots slots,
 // contracts it with the slot's expert; the teams' exact sums meet in LDS, and
 // the rescale and the sum over the ranks follow in order.  k * team <= 16.
 // Bound by its trips to memory one after another: slot, offsets, row and weights
-// (8 of 64 experts of 1024 -> 2560, 5.2 MB of weights: 5.7 us).
+// (8 of 64 experts of 1024 -> 2560, 5.2 MB of weights: 6.6 us from memory, 5.7
+// from the cache).
 template <int MODE, int U, int Q>
 __global__ __launch_bounds__(1024) void k_experts_token(const Slots slots,
                                                         const int32_t* __restrict__ slot_of,
@@ -505,7 +508,10 @@ hipError_t launch_products(const Slots& s, int64_t x_rows, const uint8_t* packed
                            const float* gamma, const float* gamma2, const int8_t* xq,
                            const float* absmax, int64_t n, int64_t k, float* y, uint16_t* h,
                            int32_t* acc, hipStream_t stream) {
-  // the tiled kernel's 32-bit offsets, and blocks of 256 threads in a grid
+  // the tiled kernel's 32-bit offsets, and blocks of 256 threads in a grid: past
+  // them the rows go to the decode kernel, 16 at a time with the weights again
+  // (64 experts of 8192 -> 2560, 8 per token, by slot: 32752 tokens 6.4 ms, 32768,
+  // where rows * K reaches 2^31, 17.7)
   const bool tiled = k >= 64 && x_rows * k < (int64_t(1) << 31) &&
                      n * (k / 16) < (int64_t(1) << 31) &&
                      (n + 127) / 128 * row_blocks(s.P, s.E, 32) < (int64_t(1) << 24) - 8;

@@ -6,10 +6,13 @@
 // per lane, as keys whose unsigned order is that of the values (0 for a masked
 // one).  A rank is a maximum over them and the lowest expert that has it, both
 // by DPP; the weights' exponentials follow once the ranks are known, lane j's
-// for rank j.  With a row per token a wave's instructions serve four tokens,
-// and instructions are what bounds this kernel (8192 tokens, 128 experts, k = 8,
-// the whole router: a wave per token with an exponential in every rank 23.5
-// us, this 12.6; 64 tokens 17.1 -> 9.5).
+// for rank j.  With a row per token a wave's instructions serve four tokens
+// (8192 tokens, 128 experts, k = 8, the whole router: a wave per token with an
+// exponential in every rank 23.5 us, this 12.6; 64 tokens 17.1 -> 9.5).  Bound by
+// latency: of that choice's 6.6 us VALU issue is 6.2 thousand cycles (2.6 us); a
+// wave lives 12 thousand, two thirds of them waiting for its logits (two bytes
+// a load) and along the DPP chains of the ranks, with two waves per SIMD to
+// cover it.
 //
 // Slots.  A block takes up to 64 tokens, whose choices of expert e are one
 // 64-bit mask: a pair's place among its expert's pairs of the block is the number of

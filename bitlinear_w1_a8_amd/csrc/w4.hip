@@ -34,7 +34,7 @@ __device__ __forceinline__ uint16_t f_bf16(float f) {   // finite f >= 0, neares
 // Four neighbouring lanes hold one block of a row: lane q its 16-byte chunk,
 // weights k = 32j + 8q + i.  A group of 32, 64 or 128 is one, two or four of
 // the j over the four lanes.  Bound by reading the weights (8192 x 28672: 0.94
-// GB in 239 us, 4.4 TB/s in and out together, a copy's 4.75).
+// GB in 246-260 us, 4.1-4.3 TB/s in and out together, a copy's 4.75).
 template <int G, bool ZEROS, typename INDEX>
 __global__ __launch_bounds__(256) void k_pack_w4(const float* __restrict__ w, INDEX units, int K,
                                                  uint4* __restrict__ packed,
@@ -104,7 +104,7 @@ __global__ __launch_bounds__(256) void k_pack_w4(const float* __restrict__ w, IN
 
 // Eight neighbouring lanes hold one block of a row, lane (q, p) the low (p = 0)
 // or high nibbles of chunk q: per word j they write 128 consecutive bytes.
-// Bound by these writes (8192 x 28672: 231 us, 4.6 TB/s in and out together).
+// Bound by these writes (8192 x 28672: 235-238 us, 4.5 TB/s in and out together).
 // INDEX: a 32-bit unsigned type where it numbers all lanes.
 template <bool ZEROS, typename INDEX>
 __global__ __launch_bounds__(256) void k_unpack_w4(const uint4* __restrict__ packed,
@@ -188,7 +188,9 @@ struct Run {
 // blocks into runs; a wave holds two buffers of U blocks (1 KiB each), one on
 // its way while it works on the other, and goes on to its next rows without a
 // pause where it is a team of its own.  Bound by the weight stream (2560 ->
-// 128256, one token: 170 MB in 32 us, 5.3 TB/s).
+// 128256, one token: 170 MB in 33.8 us, 5.0 TB/s; a pure read stream reaches
+// 6.3); with few rows by latency (6912 -> 2560, 7 tokens, groups of 32: 10.5 MB in
+// 10.8 us on 160 of 256 CUs).
 // NV: result registers in use (1: one token, 4: up to 16).
 template <int G, bool ZEROS, int NV, int U>
 __global__ __launch_bounds__(512) void k_w4_few(const uint4* __restrict__ packed,
@@ -380,9 +382,11 @@ __global__ __launch_bounds__(512) void k_w4_few(const uint4* __restrict__ packed
 //
 // A group's sums are converted and scaled in registers, two VALU operations of
 // four cycles per register and group, against 32 cycles of MFMA per 32 k and
-// fragment: for groups of 32 and 64 that, not the matrix cores, bounds the
-// kernel (2560 -> 6912, 2048 tokens, groups of 64, 69-71 us: 98 of 159 thousand
-// cycles VALU, 35 MFMA).  Zero points come off the codes (t - z fits an int8;
+// fragment: for groups of 32 and 64 that is the largest part, not the matrix
+// cores, but it does not fill the time either (2560 -> 6912, 2048 tokens, groups
+// of 64, 70 us: VALU issue 98 of 160 thousand cycles, MFMA 35; the four waves of a
+// block meet at a barrier every 128 k).  Groups of 32 / 64 / 128: 96 / 77 / 60 us
+// back to back, with zero points 106 / 89 / 72.  Zero points come off the codes (t - z fits an int8;
 // five more operations per word, which all row fragments share) and not off the
 // sums (two operations per register).
 //

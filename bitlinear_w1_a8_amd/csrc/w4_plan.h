@@ -38,12 +38,16 @@ inline W4Plan w4_plan(int64_t t, int64_t n, int64_t k, int g, int64_t cus) {
   // pass over the matrix for each lot.  k_w4_tile reads the matrix once, so it
   // has the batches that would take three passes or more, and those of two but
   // for matrices so small that their tiles leave CUs idle and K is cut over
-  // eight waves.  us, k_w4_few / k_w4_tile, 28672 -> 8192: 6 tokens (2 passes)
-  // 92.7 / 41.4, 16 (4) 174.6 / 43.0; 14336 -> 8192: 12 (2) 52.7 / 22.9; 28672 ->
-  // 4096: 6 (2) 51.0 / 36.7; 28672 -> 2560: 6 (2) 33.3 / 37.9, 10 (2) 36.9 / 39.0, 12
-  // (3) 52.2 / 39.6; 14336 -> 2560: 11 (2) 22.4 / 24.1, groups of 32 16 (2) 27.4 / 23.1;
-  // 28672 -> 1024: 10 (2) 32.3 / 35.9, 11 (3) 43.2 / 36.3; 131072 -> 1024: 2 (2) 106.8 /
-  // 145.2, 4 (4) 199.9 / 146.2; 10240 -> 128256: 16 (2) 307 / 248.
+  // eight waves.  us, k_w4_few / k_w4_tile:
+  //   one pass    2560 -> 128256, 16 tokens 41.8 / 62.3; 8192 -> 12288, 16 21.1 / 22.9;
+  //               14336 -> 8192, 8 20.6 / 22.3; 28672 -> 8192, 5 33.3 / 39.5; 14336 ->
+  //               16384, 10 35.7 / 39.4; 131072 -> 1024, 1 58.7 / 144.9
+  //   two         28672 -> 8192, 6 55.4 / 38.9; 14336 -> 8192, 12 35.2 / 22.6; 10240 ->
+  //               128256, 16 294 / 240; small ones: 28672 -> 4064, 10 36.3 / 36.9;
+  //               28672 -> 2560, 10 37.1 / 38.9; 28672 -> 1024, 10 31.7 / 35.9; 14336 ->
+  //               2560, 16 24.9 / 24.7, groups of 32 27.0 / 23.0; 131072 -> 1024, 2 105 / 146
+  //   three, four 28672 -> 8192, 11 79.8 / 40.4, 16 104.7 / 42.5; 28672 -> 2560, 12 52.4 /
+  //               39.5; 28672 -> 1024, 11 42.6 / 36.1; 131072 -> 1024, 3 150.5 / 146.1
   const int64_t most = std::min<int64_t>(16, kMaxLds / token_stride(k));
   const int64_t passes = (t + most - 1) / most, tiles16 = (n + 15) / 16;
   if (t <= 16 && (passes == 1 || (passes == 2 && tiles16 < cus))) {

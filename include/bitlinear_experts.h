@@ -92,7 +92,8 @@ bl_status bitlinear_route_experts(const void* logits, int dtype, int64_t T, int6
  *               writes them (2i gate, 2i + 1 up), 16-byte aligned.
  *   gamma_gate, gamma_up   [E] float32 each, one per expert.
  *   N, K        1 <= N <= 2^25, 16 <= K <= BITLINEAR_MAX_K, K % 16 == 0, 2 E N K <= 2^38,
- *               T * k * 2N <= 2^36.
+ *               T * k * 2N <= 2^36.  Fast up to T * K < 2^31 and 2N * K < 2^35; larger
+ *               products run some three times longer per row.
  *   h           [T * k, N] bfloat16 output (uint16 bit patterns), by slot; rows of
  *               empty slots are left as they were.
  *   xq          [T, K] int8 activations (written), 16-byte aligned.
@@ -124,7 +125,8 @@ size_t bitlinear_experts_workspace_bytes(int64_t T, int64_t k, int64_t N);
  *   packed     [E, N, K/4] from bitlinear_pack_weights, 16-byte aligned.
  *   gamma      [E] float32.
  *   N, K       1 <= N <= 2^26, 16 <= K <= BITLINEAR_MAX_K, K % 16 == 0, E N K <= 2^38,
- *              T * k * N <= 2^36.
+ *              T * k * N <= 2^36.  Fast up to (rows of x) * K < 2^31 and N * K < 2^35;
+ *              larger products run some three times longer per row (split the batch).
  *   y          float32 output, 4-byte aligned.
  *   xq         int8 activations (written), as many rows as x, 16-byte aligned.
  *   absmax     row absmax (written), one per row of x, 4-byte aligned.  In both, rows of
