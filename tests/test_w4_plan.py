@@ -109,3 +109,7 @@ def test_team_fills_the_device(plan):
                 if p.wn or p.team == 8 or -(-k // 128) <= 4 * p.team:
                     continue
                 assert -(-n // 16) * 2 * p.team / 8 > (2 if t == 1 else 1) * CUS, (t, n, k, p)
+
+
+def test_wide_cases_reach_the_larger_tiles(plan):
+    assert [plan(t, n, k, g, CUS)[:3] for t, n, k, g in w4_cases.WIDE] == [(4, 2, 1), (4, 1, 1), (4, 1, 2), (8, 1, 4)]

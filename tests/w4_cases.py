@@ -31,9 +31,11 @@ ROUNDS += [(1, 8200, 65536, 128), (1, 8200, 65568, 32)]
 PASSES = [(16, 300, 14336, 32), (11, 300, 14336, 64), (16, 300, 14400, 64), (13, 260, 14336, 128), (2, 40, 131072, 128)]
 # up to 16 tokens on the tiled kernel: longer rows than LDS has room for
 LONG = [(12, 5000, 14336, 64), (16, 9000, 12288, 128), (16, 4100, 9632, 32), (3, 33, 131072, 128)]
+# the same over so many rows that larger tiles take them, with one partial row block
+WIDE = [(16, 20000, 12288, 64), (16, 35000, 9856, 32), (16, 41000, 9728, 64), (16, 41000, 9728, 128)]
 
 FEW = TEAMS + ROUNDS + PASSES
-CASES = [(t, n, k, g) for shapes in TILED.values() for t, n, gk in shapes for g, k in gk] + FEW + LONG
+CASES = [(t, n, k, g) for shapes in TILED.values() for t, n, gk in shapes for g, k in gk] + FEW + LONG + WIDE
 
 
 def forward(packed, scales, zeros, xq, absmax):
