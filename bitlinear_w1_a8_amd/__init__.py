@@ -11,6 +11,8 @@ _EXPORTS = ("pack_weights", "quant_act", "subln_quant_act", "forward", "bitlinea
             "BitLinearError", "load", "last_error")
 _EXPERTS = ("Routing", "route_experts", "gated_relu2_experts", "linear_experts")
 _W4 = ("pack_weights_w4", "unpack_weights_w4", "forward_w4")
+_NORM = ("add_subln_quant_act", "add_subln_quant_act_f8")
+_F8 = ("quant_act_f8", "pack_weights_f8", "unpack_weights_f8", "forward_f8", "linear_f8")
 
 
 def __getattr__(name):
@@ -21,6 +23,10 @@ def __getattr__(name):
         from . import experts as module
     elif name in _W4:
         from . import w4 as module
+    elif name in _NORM:
+        from . import norm as module
+    elif name in _F8:
+        from . import f8 as module
     else:
         raise AttributeError(name)
     value = globals()[name] = getattr(module, name)   # found at once from now on

@@ -1,0 +1,121 @@
+"""Linear layers in 8-bit floating point with a scale for each block of 128
+(include/bitlinear_f8.h), same names.  Argument marshalling only, as
+``binding``."""
+
+import torch
+
+from . import binding
+from ._marshal import call, device_of, need
+from .binding import BL_BF16, BL_F32, _c_i64, _c_int, _c_vp
+
+# name -> (restype, argtypes), as declared in include/bitlinear_f8.h
+SIGNATURES = {
+    "bitlinear_quant_act_f8": (_c_int, [_c_vp, _c_int, _c_i64, _c_i64, _c_vp, _c_vp, _c_vp]),
+    "bitlinear_pack_weights_f8": (_c_int, [_c_vp, _c_i64, _c_i64, _c_vp, _c_vp, _c_vp]),
+    "bitlinear_unpack_weights_f8": (_c_int, [_c_vp, _c_vp, _c_i64, _c_i64, _c_vp, _c_vp]),
+    "bitlinear_forward_f8": (_c_int, [_c_vp, _c_vp, _c_vp, _c_vp, _c_i64, _c_i64, _c_i64, _c_vp,
+                                      _c_int, _c_vp]),
+}
+
+_DTYPES = {torch.float32: BL_F32, torch.bfloat16: BL_BF16}
+_F8 = torch.float8_e4m3fn
+
+_lib = None
+
+
+def _load():
+    global _lib
+    if _lib is None:
+        _lib = binding.declare(SIGNATURES)
+    return _lib
+
+
+def _blocks(n):
+    return (n + 127) // 128
+
+
+def _matrix(dev, w, w_scales):
+    """Checks a matrix; returns its shape."""
+    if w.dim() != 2:
+        raise ValueError("w must be [N, K]")
+    n, k = shape = w.shape
+    need(dev, w, "w", _F8, shape)
+    need(dev, w_scales, "w_scales", torch.float32, (_blocks(n), _blocks(k)))
+    return n, k
+
+
+def quant_act_f8(x):
+    """x [T, K] (float32 or bfloat16) -> (xq float8_e4m3fn [T, K], scales
+    float32 [ceil(K / 128), T]), one scale per token and 128 features."""
+    lib = _load()
+    dev = device_of(x, "x")
+    dt = _DTYPES.get(x.dtype)
+    if dt is None:
+        raise TypeError(f"x must be float32 or bfloat16, got {x.dtype}")
+    if x.dim() != 2:
+        raise ValueError("x must be [T, K]")
+    t, k = shape = x.shape
+    need(dev, x, "x", x.dtype, shape)
+    xq = torch.empty(shape, dtype=_F8, device=x.device)
+    scales = torch.empty((_blocks(k), t), dtype=torch.float32, device=x.device)
+    call(dev, lib.bitlinear_quant_act_f8, x.data_ptr(), dt, t, k, xq.data_ptr(), scales.data_ptr())
+    return xq, scales
+
+
+def pack_weights_f8(w):
+    """float32 w [N, K] -> (codes float8_e4m3fn [N, K], scales float32
+    [ceil(N / 128), ceil(K / 128)]), one scale per block of 128 x 128."""
+    lib = _load()
+    dev = device_of(w, "w")
+    if w.dim() != 2:
+        raise ValueError("w must be [N, K]")
+    n, k = shape = w.shape
+    need(dev, w, "w", torch.float32, shape)
+    codes = torch.empty(shape, dtype=_F8, device=w.device)
+    scales = torch.empty((_blocks(n), _blocks(k)), dtype=torch.float32, device=w.device)
+    call(dev, lib.bitlinear_pack_weights_f8, w.data_ptr(), n, k, codes.data_ptr(), scales.data_ptr())
+    return codes, scales
+
+
+def unpack_weights_f8(w, w_scales):
+    """The float32 values [N, K] that a matrix of pack_weights_f8 stands for."""
+    lib = _load()
+    dev = device_of(w, "w")
+    n, k = _matrix(dev, w, w_scales)
+    out = torch.empty((n, k), dtype=torch.float32, device=w.device)
+    call(dev, lib.bitlinear_unpack_weights_f8, w.data_ptr(), w_scales.data_ptr(), n, k, out.data_ptr())
+    return out
+
+
+def forward_f8(w, w_scales, xq, x_scales, dtype=torch.float32, out=None):
+    """y [T, N] of ``dtype`` (float32 or bfloat16; ``out`` brings its own) =
+    tokens (xq float8_e4m3fn [T, K], x_scales float32 [ceil(K / 128), T], from
+    quant_act_f8 or add_subln_quant_act_f8) times a matrix of pack_weights_f8."""
+    lib = _load()
+    dev = device_of(xq, "xq")
+    device_of(w, "w")
+    if xq.dim() != 2:
+        raise ValueError("xq must be [T, K]")
+    t, k = shape = xq.shape
+    n = w.shape[0] if w.dim() == 2 else 0
+    need(dev, xq, "xq", _F8, shape)
+    need(dev, w, "w", _F8, (n, k))
+    need(dev, w_scales, "w_scales", torch.float32, (_blocks(n), _blocks(k)))
+    need(dev, x_scales, "x_scales", torch.float32, (_blocks(k), t))
+    if out is None:
+        if dtype not in _DTYPES:
+            raise TypeError(f"dtype must be float32 or bfloat16, got {dtype}")
+        out = torch.empty((t, n), dtype=dtype, device=xq.device)
+    else:
+        device_of(out, "out")
+        if out.dtype not in _DTYPES:
+            raise TypeError(f"out must be float32 or bfloat16, got {out.dtype}")
+        need(dev, out, "out", out.dtype, (t, n))
+    call(dev, lib.bitlinear_forward_f8, w.data_ptr(), w_scales.data_ptr(), xq.data_ptr(),
+         x_scales.data_ptr(), t, n, k, out.data_ptr(), _DTYPES[out.dtype])
+    return out
+
+
+def linear_f8(x, w, w_scales, dtype=torch.float32, out=None):
+    """Quantise x [T, K] (float32 or bfloat16) and multiply: y [T, N]."""
+    return forward_f8(w, w_scales, *quant_act_f8(x), dtype=dtype, out=out)
