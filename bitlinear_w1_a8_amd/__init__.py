@@ -9,7 +9,7 @@ _EXPORTS = ("pack_weights", "quant_act", "subln_quant_act", "forward", "bitlinea
             "interleave_rows", "gated_relu2", "pack_weights_binary", "forward_binary",
             "gemv_max_tokens",
             "BitLinearError", "load", "last_error")
-_EXPERTS = ("Routing", "route_experts", "gated_relu2_experts", "linear_experts")
+_EXPERTS = ("Routing", "route_experts", "gated_relu2_experts", "linear_experts", "experts_ffn")
 _W4 = ("pack_weights_w4", "unpack_weights_w4", "forward_w4")
 _NORM = ("add_subln_quant_act", "add_subln_quant_act_f8")
 _F8 = ("quant_act_f8", "pack_weights_f8", "unpack_weights_f8", "forward_f8", "linear_f8")

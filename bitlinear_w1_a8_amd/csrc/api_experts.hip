@@ -143,6 +143,56 @@ bl_status bitlinear_linear_experts(const bl_routing* routing, const void* x, int
                                                 static_cast<hipStream_t>(stream)));
 }
 
+size_t bitlinear_experts_ffn_workspace_bytes(int64_t T, int64_t E, int64_t k, int64_t F, int64_t K,
+                                             int64_t N) {
+  if (T < 1 || T > kMaxT || E < 1 || E > BITLINEAR_MAX_EXPERTS || k < 1 || k > BITLINEAR_MAX_TOP_K ||
+      F < 1 || F > BITLINEAR_MAX_K || K < 1 || K > BITLINEAR_MAX_K || N < 1 || N > kMaxN ||
+      T * k > kMaxTN / N || T * k > kMaxTN / (2 * F))
+    return 0;
+  return bl::layer_workspace_bytes(T, E, k, F, K, N);
+}
+
+bl_status bitlinear_experts_ffn(const void* logits, int logits_dtype, int64_t T, int64_t E,
+                                int64_t k, int share, const void* x, int x_dtype,
+                                const float* absmax, const uint8_t* packed_gu,
+                                const float* gamma_gate, const float* gamma_up, int64_t F,
+                                int64_t K, const uint8_t* packed_down, const float* gamma_down,
+                                int64_t N, float* y, void* workspace, size_t workspace_bytes,
+                                void* stream) {
+  const char* fn = "bitlinear_experts_ffn";
+  if (!logits || !x || !packed_gu || !gamma_gate || !gamma_up || !packed_down || !gamma_down || !y ||
+      !workspace || (x_dtype == BL_CODES && !absmax))
+    return fail(BL_ERR_NULL, "%s: NULL pointer argument", fn);
+  if (logits_dtype != BL_F32 && logits_dtype != BL_BF16)
+    return fail(BL_ERR_DTYPE, "%s: unknown logits_dtype %d", fn, logits_dtype);
+  if (x_dtype != BL_F32 && x_dtype != BL_BF16 && x_dtype != BL_CODES)
+    return fail(BL_ERR_DTYPE, "%s: unknown x_dtype %d", fn, x_dtype);
+  if (x_dtype != BL_CODES && absmax)
+    return fail(BL_ERR_ARG, "%s: absmax belongs to int8 codes (BL_CODES)", fn);
+  if (bl_status rc = check_counts(fn, T, k, E)) return rc;
+  if (share != BL_SHARE_CHOSEN && share != BL_SHARE_ALL)
+    return fail(BL_ERR_ARG, "%s: unknown share %d (BL_SHARE_CHOSEN or BL_SHARE_ALL)", fn, share);
+  if (bl_status rc = check_k(fn, K)) return rc;
+  if (bl_status rc = check_k(fn, F)) return rc;
+  if (2 * F * K > kMaxNK / E || T * k > kMaxTN / (2 * F))
+    return fail(BL_ERR_SHAPE, "%s: F=%lld out of range", fn, (long long)F);
+  if (N < 1 || N > kMaxN || N * F > kMaxNK / E || T * k > kMaxTN / N)
+    return fail(BL_ERR_SHAPE, "%s: N=%lld out of range", fn, (long long)N);
+  if (!aligned(x, 16) || !aligned(packed_gu, 16) || !aligned(packed_down, 16) ||
+      !aligned(workspace, 16) || !aligned(logits, logits_dtype == BL_F32 ? 4 : 2) ||
+      !aligned(absmax, 4) || !aligned(gamma_gate, 4) || !aligned(gamma_up, 4) ||
+      !aligned(gamma_down, 4) || !aligned(y, 4))
+    return fail(BL_ERR_ALIGN, "%s: x, the packed matrices and workspace need 16-byte, logits their "
+                "dtype's, the others 4-byte alignment", fn);
+  const size_t need = bl::layer_workspace_bytes(T, E, k, F, K, N);
+  if (workspace_bytes < need)
+    return fail(BL_ERR_WORKSPACE, "%s: workspace of %zu bytes, need %zu", fn, workspace_bytes, need);
+  return launched(fn, bl::launch_layer({logits, x, absmax, packed_gu, packed_down, gamma_gate,
+                                        gamma_up, gamma_down, T, E, k, F, K, N, y, workspace,
+                                        logits_dtype == BL_BF16, share, x_dtype},
+                                       static_cast<hipStream_t>(stream)));
+}
+
 int64_t bitlinear_w4_row_bytes(int64_t K) { return K < 1 ? 0 : bl::w4_row_bytes(K); }
 
 bl_status bitlinear_pack_weights_w4(const float* w, int64_t N, int64_t K, int64_t G,

@@ -158,10 +158,34 @@ hipError_t launch_gated_experts(const bl_routing& r, const void* x, int bf16, co
                                 const float* gamma_gate, const float* gamma_up, int64_t n,
                                 int64_t k, uint16_t* h, int8_t* xq, float* absmax, int32_t* acc,
                                 hipStream_t stream);   // n: rows of gate and up together
+// The same of int8 rows, one per token.
+hipError_t launch_gated_codes(const bl_routing& r, const int8_t* xq, const float* absmax,
+                              const uint8_t* packed, const float* gamma_gate,
+                              const float* gamma_up, int64_t n, int64_t k, uint16_t* h,
+                              hipStream_t stream);
 hipError_t launch_linear_experts(const bl_routing& r, const void* x, int bf16, int x_rows,
                                  const uint8_t* packed, const float* gamma, int64_t n, int64_t k,
                                  float* y, int y_rows, int8_t* xq, float* absmax, int32_t* acc,
                                  float* workspace, hipStream_t stream);
+
+// ---------------------------------------------------------------- whole layer (layer.hip)
+
+struct LayerCall {
+  const void* logits;
+  const void* x;                     // x_dtype BL_F32, BL_BF16 or BL_CODES
+  const float* absmax;               // of codes
+  const uint8_t* gu;
+  const uint8_t* down;
+  const float* gamma_gate;
+  const float* gamma_up;
+  const float* gamma_down;
+  int64_t T, E, k, F, K, N;
+  float* y;
+  void* workspace;
+  int logits_bf16, share, x_dtype;
+};
+size_t layer_workspace_bytes(int64_t t, int64_t e, int64_t k, int64_t f, int64_t kk, int64_t n);
+hipError_t launch_layer(const LayerCall& c, hipStream_t stream);
 
 // ---------------------------------------------------------------- 4-bit weights (w4.hip)
 

@@ -1,5 +1,6 @@
 """Routed experts (include/bitlinear_experts.h), same names: the router, the
-experts' gated feed-forward half and their linear layers.
+experts' gated feed-forward half, their linear layers, and all three as one
+layer.
 
 Argument marshalling only, as ``binding``: tensors are allocated with torch on
 the caller's device and every step runs in the library's HIP kernels on the
@@ -21,6 +22,7 @@ MAX_EXPERTS, MAX_TOP_K = 1024, 32
 SHARES = {"chosen": 0, "all": 1}
 _TOKENS, _SLOTS = 0, 1                       # bl_rows
 _DTYPES = {torch.float32: BL_F32, torch.bfloat16: BL_BF16}
+_CODES = 2                                   # BL_CODES
 
 
 #: struct bl_routing: T, k, E, then the pointers offsets, pairs, slots, weights
@@ -37,6 +39,10 @@ SIGNATURES = {
     "bitlinear_linear_experts": (_c_int, [_c_vp, _c_vp, _c_int, _c_int, _c_vp, _c_vp, _c_i64,
                                           _c_i64, _c_vp, _c_int, _c_vp, _c_vp, _c_vp, _c_vp, _c_sz,
                                           _c_vp]),
+    "bitlinear_experts_ffn_workspace_bytes": (_c_sz, [_c_i64] * 6),
+    "bitlinear_experts_ffn": (_c_int, [_c_vp, _c_int, _c_i64, _c_i64, _c_i64, _c_int, _c_vp, _c_int,
+                                       _c_vp, _c_vp, _c_vp, _c_vp, _c_i64, _c_i64, _c_vp, _c_vp,
+                                       _c_i64, _c_vp, _c_vp, _c_sz, _c_vp]),
 }
 
 _lib = None
@@ -210,3 +216,60 @@ def linear_experts(x, packed, gamma, routing, combine=True, x_rows="slots", want
          packed.data_ptr(), gamma.data_ptr(), n, kk, y.data_ptr(), _TOKENS if combine else _SLOTS,
          at, at + a, acc.data_ptr() if want_acc else None, at + a + b if combine else None, wsb)
     return (y, acc) if want_acc else y
+
+
+def experts_ffn(x, logits, k, packed_gu, gamma_gate, gamma_up, packed_down, gamma_down, absmax=None,
+                share="chosen", out=None):
+    """A whole routed layer, the same bits as route_experts, gated_relu2_experts
+    and linear_experts one after the other; for up to 16 tokens in two launches
+    (three where more than 4 tokens are not quantised yet).
+
+    x [T, K]: float32 or bfloat16, or int8 codes with their ``absmax`` float32
+    [T] (quant_act, subln_quant_act, add_subln_quant_act); logits [T, E] (float32
+    or bfloat16); packed_gu uint8 [E, 2F, K/4], each expert's rows from
+    interleave_rows; packed_down uint8 [E, N, F/4]; the gammas float32 [E].
+    Returns y float32 [T, N]."""
+    lib = _load()
+    dev = device_of(x, "x")
+    if x.dtype is torch.int8:
+        if absmax is None:
+            raise ValueError("int8 codes need their absmax")
+        dt = _CODES
+    else:
+        dt = _DTYPES.get(x.dtype)
+        if dt is None:
+            raise TypeError(f"x must be float32, bfloat16 or int8 codes, got {x.dtype}")
+        if absmax is not None:
+            raise ValueError("absmax belongs to int8 codes")
+    device_of(logits, "logits")
+    lt = _DTYPES.get(logits.dtype)
+    if lt is None:
+        raise TypeError(f"logits must be float32 or bfloat16, got {logits.dtype}")
+    if x.dim() != 2 or logits.dim() != 2 or packed_gu.dim() != 3 or packed_down.dim() != 3:
+        raise ValueError("x must be [T, K], logits [T, E], packed_gu [E, 2F, K/4], packed_down [E, N, F/4]")
+    if share not in SHARES:
+        raise ValueError(f"share must be one of {sorted(SHARES)}, got {share!r}")
+    t, kk = shape = x.shape
+    e = logits.shape[1]
+    f, n = packed_gu.shape[1] // 2, packed_down.shape[1]
+    k = operator.index(k)
+    if not 1 <= k <= MAX_TOP_K:
+        raise ValueError(f"k must be in [1, {MAX_TOP_K}], got {k}")
+    need(dev, x, "x", x.dtype, shape)
+    need(dev, logits, "logits", logits.dtype, (t, e))
+    need(dev, packed_gu, "packed_gu", torch.uint8, (e, 2 * f, kk // 4))
+    need(dev, packed_down, "packed_down", torch.uint8, (e, n, f // 4))
+    need(dev, gamma_gate, "gamma_gate", torch.float32, (e,))
+    need(dev, gamma_up, "gamma_up", torch.float32, (e,))
+    need(dev, gamma_down, "gamma_down", torch.float32, (e,))
+    if absmax is not None:
+        need(dev, absmax, "absmax", torch.float32, (t,))
+    on = x.device
+    y = _out(dev, out, (t, n), torch.float32, on)
+    wsb = lib.bitlinear_experts_ffn_workspace_bytes(t, e, k, f, kk, n)
+    ws = torch.empty(wsb, dtype=torch.uint8, device=on)
+    call(dev, lib.bitlinear_experts_ffn, logits.data_ptr(), lt, t, e, k, SHARES[share], x.data_ptr(),
+         dt, None if absmax is None else absmax.data_ptr(), packed_gu.data_ptr(),
+         gamma_gate.data_ptr(), gamma_up.data_ptr(), f, kk, packed_down.data_ptr(),
+         gamma_down.data_ptr(), n, y.data_ptr(), ws.data_ptr(), wsb)
+    return y

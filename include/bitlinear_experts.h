@@ -41,6 +41,10 @@ typedef enum {
   BL_ROWS_SLOTS = 1   /* one row per slot: [T * k, .] */
 } bl_rows;
 
+/* Activations that are step A1's int8 codes already, with their absmax beside
+ * them (argument `x_dtype` of bitlinear_experts_ffn, next to bl_dtype's). */
+#define BL_CODES 2
+
 /* Where a batch of tokens goes: a HOST struct of device pointers, as
  * bitlinear_route_experts fills the arrays.  The kernels keep every access in
  * bounds whatever the arrays hold (offsets are taken as lying in [0, T * k]
@@ -142,6 +146,40 @@ bl_status bitlinear_linear_experts(const bl_routing* routing, const void* x, int
                                    int64_t N, int64_t K, float* y, int y_rows, int8_t* xq,
                                    float* absmax, int32_t* acc, void* workspace,
                                    size_t workspace_bytes, void* stream);
+
+/* Bytes of device workspace that bitlinear_experts_ffn needs. */
+size_t bitlinear_experts_ffn_workspace_bytes(int64_t T, int64_t E, int64_t k, int64_t F, int64_t K,
+                                             int64_t N);
+
+/* A whole routed feed-forward layer: bitlinear_route_experts of the logits,
+ * bitlinear_gated_relu2_experts of the tokens and bitlinear_linear_experts of
+ * its rows with the weighted sum, the same bits.  A few tokens (up to 16, with
+ * k <= 16 and E <= 256) take two launches, three where more than 4 of them are
+ * not quantised yet; more tokens take the three calls' launches.
+ *
+ *   logits, logits_dtype, T, E, k, share   as bitlinear_route_experts.
+ *   x           [T, K]: activations of dtype BL_F32 or BL_BF16, or (BL_CODES) step
+ *               A1's int8 codes as bitlinear_quant_act, bitlinear_subln_quant_act or
+ *               bitlinear_add_subln_quant_act write them; 16-byte aligned.
+ *   absmax      [T] float32 with BL_CODES, as the same call wrote it; else NULL.
+ *   packed_gu, gamma_gate, gamma_up        as bitlinear_gated_relu2_experts, F rows each:
+ *               [E, 2F, K/4], [E], [E].
+ *   packed_down, gamma_down                as bitlinear_linear_experts: [E, N, F/4], [E].
+ *   F, K, N     F and K multiples of 16 in [16, BITLINEAR_MAX_K]; F as N of
+ *               bitlinear_gated_relu2_experts, N as N of bitlinear_linear_experts.
+ *   y           [T, N] float32 output, 4-byte aligned.
+ *   workspace   device scratch, 16-byte aligned, of at least
+ *               bitlinear_experts_ffn_workspace_bytes(T, E, k, F, K, N) bytes;
+ *               overwritten.  Calls that may overlap need one each.
+ * Errors: BL_ERR_NULL, BL_ERR_SHAPE, BL_ERR_ALIGN, BL_ERR_DTYPE, BL_ERR_ARG
+ * (share, or absmax without codes), BL_ERR_WORKSPACE, BL_ERR_HIP. */
+bl_status bitlinear_experts_ffn(const void* logits, int logits_dtype, int64_t T, int64_t E,
+                                int64_t k, int share, const void* x, int x_dtype,
+                                const float* absmax, const uint8_t* packed_gu,
+                                const float* gamma_gate, const float* gamma_up, int64_t F,
+                                int64_t K, const uint8_t* packed_down, const float* gamma_down,
+                                int64_t N, float* y, void* workspace, size_t workspace_bytes,
+                                void* stream);
 
 #ifdef __cplusplus
 }
