@@ -53,6 +53,22 @@ bl_status norm(const char* fn, const bl::NormCall& c, int x_dtype, int r_dtype, 
   return launched(fn, bl::launch_add_subln(c, stream));
 }
 
+bl_status check_product(const char* fn, const uint8_t* w, const float* w_scales, const uint8_t* xq,
+                        const float* x_scales, int64_t t, int64_t n, int64_t k, const void* y,
+                        int y_dtype) {
+  if (!w || !w_scales || !xq || !x_scales || !y)
+    return fail(BL_ERR_NULL, "%s: NULL pointer argument", fn);
+  if (bl_status rc = check_dtype(fn, "y_dtype", y_dtype)) return rc;
+  if (bl_status rc = check_matrix(fn, n, k)) return rc;
+  if (t < 1 || t > kMaxT || t > kMaxTN / n)
+    return fail(BL_ERR_SHAPE, "%s: T=%lld out of range", fn, (long long)t);
+  if (!aligned(w, 16) || !aligned(xq, 16) || !aligned(w_scales, 4) || !aligned(x_scales, 4) ||
+      !aligned(y, y_dtype == BL_F32 ? 4 : 2))
+    return fail(BL_ERR_ALIGN, "%s: w and xq need 16-byte, the scales 4-byte alignment, y its "
+                "element's", fn);
+  return BL_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -113,18 +129,24 @@ bl_status bitlinear_forward_f8(const uint8_t* w, const float* w_scales, const ui
                                const float* x_scales, int64_t T, int64_t N, int64_t K, void* y,
                                int y_dtype, void* stream) {
   const char* fn = "bitlinear_forward_f8";
-  if (!w || !w_scales || !xq || !x_scales || !y)
-    return fail(BL_ERR_NULL, "%s: NULL pointer argument", fn);
-  if (bl_status rc = check_dtype(fn, "y_dtype", y_dtype)) return rc;
-  if (bl_status rc = check_matrix(fn, N, K)) return rc;
-  if (T < 1 || T > kMaxT || T > kMaxTN / N)
-    return fail(BL_ERR_SHAPE, "%s: T=%lld out of range", fn, (long long)T);
-  if (!aligned(w, 16) || !aligned(xq, 16) || !aligned(w_scales, 4) || !aligned(x_scales, 4) ||
-      !aligned(y, y_dtype == BL_F32 ? 4 : 2))
-    return fail(BL_ERR_ALIGN, "%s: w and xq need 16-byte, the scales 4-byte alignment, y its "
-                "element's", fn);
+  if (bl_status rc = check_product(fn, w, w_scales, xq, x_scales, T, N, K, y, y_dtype)) return rc;
   return launched(fn, bl::launch_forward_f8(w, w_scales, xq, x_scales, T, N, K, y, y_dtype == BL_BF16,
                                             static_cast<hipStream_t>(stream)));
+}
+
+bl_status bitlinear_linear_f8(const void* x, int x_dtype, const uint8_t* w, const float* w_scales,
+                              int64_t T, int64_t N, int64_t K, uint8_t* xq, float* x_scales,
+                              void* y, int y_dtype, void* stream) {
+  const char* fn = "bitlinear_linear_f8";
+  if (!x) return fail(BL_ERR_NULL, "%s: NULL pointer argument", fn);
+  if (bl_status rc = check_dtype(fn, "x_dtype", x_dtype)) return rc;
+  if (bl_status rc = check_product(fn, w, w_scales, xq, x_scales, T, N, K, y, y_dtype)) return rc;
+  if (!aligned(x, 16)) return fail(BL_ERR_ALIGN, "%s: x needs 16-byte alignment", fn);
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  hipError_t e = bl::launch_quant_f8(x, x_dtype == BL_BF16, T, K, xq, x_scales, s);
+  if (e == hipSuccess)
+    e = bl::launch_forward_f8(w, w_scales, xq, x_scales, T, N, K, y, y_dtype == BL_BF16, s);
+  return launched(fn, e);
 }
 
 }  // extern "C"

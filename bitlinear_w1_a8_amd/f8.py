@@ -15,6 +15,8 @@ SIGNATURES = {
     "bitlinear_unpack_weights_f8": (_c_int, [_c_vp, _c_vp, _c_i64, _c_i64, _c_vp, _c_vp]),
     "bitlinear_forward_f8": (_c_int, [_c_vp, _c_vp, _c_vp, _c_vp, _c_i64, _c_i64, _c_i64, _c_vp,
                                       _c_int, _c_vp]),
+    "bitlinear_linear_f8": (_c_int, [_c_vp, _c_int, _c_vp, _c_vp, _c_i64, _c_i64, _c_i64, _c_vp, _c_vp,
+                                     _c_vp, _c_int, _c_vp]),
 }
 
 _DTYPES = {torch.float32: BL_F32, torch.bfloat16: BL_BF16}
@@ -87,35 +89,65 @@ def unpack_weights_f8(w, w_scales):
     return out
 
 
+def _out(dev, out, shape, dtype, on):
+    if out is None:
+        if dtype not in _DTYPES:
+            raise TypeError(f"dtype must be float32 or bfloat16, got {dtype}")
+        return torch.empty(shape, dtype=dtype, device=on)
+    device_of(out, "out")
+    if out.dtype not in _DTYPES:
+        raise TypeError(f"out must be float32 or bfloat16, got {out.dtype}")
+    need(dev, out, "out", out.dtype, shape)
+    return out
+
+
+def _rows(w, k):
+    """Rows of a matrix of k columns."""
+    device_of(w, "w")
+    if w.dim() != 2 or w.shape[1] != k:
+        raise ValueError(f"w must be [N, {k}], got {tuple(w.shape)}")
+    return w.shape[0]
+
+
 def forward_f8(w, w_scales, xq, x_scales, dtype=torch.float32, out=None):
     """y [T, N] of ``dtype`` (float32 or bfloat16; ``out`` brings its own) =
     tokens (xq float8_e4m3fn [T, K], x_scales float32 [ceil(K / 128), T], from
     quant_act_f8 or add_subln_quant_act_f8) times a matrix of pack_weights_f8."""
     lib = _load()
     dev = device_of(xq, "xq")
-    device_of(w, "w")
     if xq.dim() != 2:
         raise ValueError("xq must be [T, K]")
     t, k = shape = xq.shape
-    n = w.shape[0] if w.dim() == 2 else 0
+    n = _rows(w, k)
     need(dev, xq, "xq", _F8, shape)
     need(dev, w, "w", _F8, (n, k))
     need(dev, w_scales, "w_scales", torch.float32, (_blocks(n), _blocks(k)))
     need(dev, x_scales, "x_scales", torch.float32, (_blocks(k), t))
-    if out is None:
-        if dtype not in _DTYPES:
-            raise TypeError(f"dtype must be float32 or bfloat16, got {dtype}")
-        out = torch.empty((t, n), dtype=dtype, device=xq.device)
-    else:
-        device_of(out, "out")
-        if out.dtype not in _DTYPES:
-            raise TypeError(f"out must be float32 or bfloat16, got {out.dtype}")
-        need(dev, out, "out", out.dtype, (t, n))
+    out = _out(dev, out, (t, n), dtype, xq.device)
     call(dev, lib.bitlinear_forward_f8, w.data_ptr(), w_scales.data_ptr(), xq.data_ptr(),
          x_scales.data_ptr(), t, n, k, out.data_ptr(), _DTYPES[out.dtype])
     return out
 
 
 def linear_f8(x, w, w_scales, dtype=torch.float32, out=None):
-    """Quantise x [T, K] (float32 or bfloat16) and multiply: y [T, N]."""
-    return forward_f8(w, w_scales, *quant_act_f8(x), dtype=dtype, out=out)
+    """quant_act_f8 of x [T, K] (float32 or bfloat16), then forward_f8: y [T, N]."""
+    lib = _load()
+    dev = device_of(x, "x")
+    dt = _DTYPES.get(x.dtype)
+    if dt is None:
+        raise TypeError(f"x must be float32 or bfloat16, got {x.dtype}")
+    if x.dim() != 2:
+        raise ValueError("x must be [T, K]")
+    t, k = shape = x.shape
+    n, blocks = _rows(w, k), _blocks(k)
+    need(dev, x, "x", x.dtype, shape)
+    need(dev, w, "w", _F8, (n, k))
+    need(dev, w_scales, "w_scales", torch.float32, (_blocks(n), blocks))
+    on = x.device
+    out = _out(dev, out, (t, n), dtype, on)
+    codes = (t * k + 255) & ~255                # the codes, then their scales, in one piece
+    scratch = torch.empty(codes + 4 * blocks * t, dtype=torch.uint8, device=on)
+    at = scratch.data_ptr()
+    call(dev, lib.bitlinear_linear_f8, x.data_ptr(), dt, w.data_ptr(), w_scales.data_ptr(), t, n, k, at,
+         at + codes, out.data_ptr(), _DTYPES[out.dtype])
+    return out

@@ -62,8 +62,12 @@ bl_status bitlinear_unpack_weights_f8(const uint8_t* codes, const float* scales,
 
 /* y[t, n] = sum over blocks g of (x_scales[g, t] * w_scales[n / 128, g])
  *           * sum_{k in g} xq[t, k] * w[n, k].
- * Sums in binary32, in an order that depends on the shape alone: the same
- * inputs give the same bits on every call.
+ * BL_F32 outputs: products and sums in binary32.  BL_BF16 outputs of more than
+ * 32 tokens may be formed by matrix instructions that cut each product of eight
+ * neighbouring k at 2^-13 of the largest of the eight, so within 7 * 2^-13 of the
+ * sum of the products' magnitudes (4e-5 to 5e-5 of the result in the norm), before
+ * they are rounded.  Sums go in an order that depends on the shape alone: the
+ * same inputs give the same bits on every call.
  *
  *   w, w_scales   as bitlinear_pack_weights_f8 writes them.
  *   xq, x_scales  as bitlinear_quant_act_f8 writes them; both code arrays 16-byte aligned.
@@ -74,6 +78,16 @@ bl_status bitlinear_unpack_weights_f8(const uint8_t* codes, const float* scales,
 bl_status bitlinear_forward_f8(const uint8_t* w, const float* w_scales, const uint8_t* xq,
                                const float* x_scales, int64_t T, int64_t N, int64_t K, void* y,
                                int y_dtype, void* stream);
+
+/* bitlinear_quant_act_f8 of x, then bitlinear_forward_f8: the same results.
+ *
+ *   x, x_dtype   as bitlinear_quant_act_f8.
+ *   w, w_scales, T, N, K, y, y_dtype   as bitlinear_forward_f8.
+ *   xq, x_scales   the tokens' codes and scales (written), as bitlinear_quant_act_f8.
+ * Errors: as the two calls, before either is made. */
+bl_status bitlinear_linear_f8(const void* x, int x_dtype, const uint8_t* w, const float* w_scales,
+                              int64_t T, int64_t N, int64_t K, uint8_t* xq, float* x_scales,
+                              void* y, int y_dtype, void* stream);
 
 #ifdef __cplusplus
 }

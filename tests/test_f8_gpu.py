@@ -17,6 +17,7 @@ import pytest
 import torch
 
 from oracle import f8_ref as ref
+from tests.f8_cases import SHAPES
 
 pytestmark = pytest.mark.gpu
 
@@ -101,12 +102,6 @@ def _cuda(w, ws, x, xs):
             torch.from_numpy(x).cuda().view(F8), torch.from_numpy(xs).cuda())
 
 
-SHAPES = [(1, 1, 16), (1, 16, 128), (2, 17, 144), (3, 33, 112), (16, 130, 272), (1, 300, 2560), (15, 64, 640),
-          (17, 257, 384), (32, 32, 1024), (33, 100, 400), (48, 129, 2576), (64, 96, 6912), (65, 128, 128),
-          (66, 1, 16), (127, 255, 144), (128, 128, 1024), (129, 130, 2064), (300, 640, 400), (512, 384, 768),
-          (257, 513, 6912), (1000, 72, 512), (4, 5000, 28672), (70, 1030, 16384)]
-
-
 @pytest.mark.parametrize("t,n,k", SHAPES)
 def test_product(bl, t, n, k):
     host = _operands(t, n, k)
@@ -164,6 +159,20 @@ def test_neighbours_untouched(bl, t, n, k, dtype):
     bl.forward_f8(w, ws, x, xs, out=buf[1:-1])
     assert torch.all(buf[0] == 7) and torch.all(buf[-1] == 7)
     assert torch.equal(buf[1:-1], bl.forward_f8(w, ws, x, xs, dtype=dtype))
+
+
+@pytest.mark.parametrize("t,n,k", [(1, 100, 144), (20, 40, 272), (130, 6002, 128), (300, 16504, 128), (1100, 8200, 128)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_output_at_any_element(bl, t, n, k, dtype):
+    """y is aligned to its element only, and nothing around it is written."""
+    w, ws, x, xs = _cuda(*_operands(t, n, k))
+    buf = torch.full((t * n + 16,), 7.0, dtype=dtype, device="cuda")
+    for at in (1, 3):
+        y = buf[at:at + t * n].view(t, n)
+        bl.forward_f8(w, ws, x, xs, out=y)
+        assert torch.equal(y, bl.forward_f8(w, ws, x, xs, dtype=dtype))
+        assert torch.all(buf[:at] == 7) and torch.all(buf[at + t * n:] == 7)
+        buf[:] = 7
 
 
 def test_infinite_token_scale_stays_in_its_row(bl):

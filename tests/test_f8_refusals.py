@@ -93,6 +93,11 @@ def test_forward_refusals(lib, kw, code):
         return lib.bitlinear_forward_f8(w, ws, x, xs, t, n, k, y, yd, None)
     assert call(**kw) == code
 
+    def linear(w=A16, ws=A16, x=A16, xs=A16, t=2, n=16, k=128, y=A16, yd=0, raw=A16, rd=1):
+        return lib.bitlinear_linear_f8(raw, rd, w, ws, t, n, k, x, xs, y, yd, None)
+    assert linear(**kw) == code
+    assert linear(raw=None) == BL_ERR_NULL and linear(rd=2) == BL_ERR_DTYPE and linear(raw=A16 + 8) == BL_ERR_ALIGN
+
 
 # ------------------------------------------------------------ binding
 
@@ -162,6 +167,18 @@ def test_f8_binding(mods):
         f8.forward_f8(w, ws, x, xs, out=torch.zeros(5, 130, dtype=torch.float16))
     with pytest.raises(ValueError):
         f8.forward_f8(w, ws, x, xs, out=torch.zeros(5, 131))
+    raw = torch.zeros(5, 144)
+    for bad in ((raw.half(), w, ws), (raw, w.float(), ws), (raw, w, ws.bfloat16())):
+        with pytest.raises(TypeError):
+            f8.linear_f8(*bad)
+    for bad in ((raw[0], w, ws), (raw[:, :128].contiguous(), w, ws), (raw, w, ws[:1]), (raw, w[0], ws),
+                (torch.zeros(144, 5).t(), w, ws)):
+        with pytest.raises(ValueError):
+            f8.linear_f8(*bad)
+    with pytest.raises(TypeError):
+        f8.linear_f8(raw, w, ws, dtype=torch.float16)
+    with pytest.raises(ValueError):
+        f8.linear_f8(raw, w, ws, out=torch.zeros(4, 130))
     with pytest.raises(TypeError):
         f8.quant_act_f8(torch.zeros(3, 64, dtype=torch.float16))
     with pytest.raises(ValueError):
