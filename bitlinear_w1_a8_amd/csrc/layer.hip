@@ -229,9 +229,9 @@ __global__ __launch_bounds__(512) void k_layer_gate(const Router rt,
 }
 
 // Down projections and the weighted sum (as k_experts_token): a block has one
-// token and 16 outputs, each of its k rows of h a team of `team` waves that
+// token and 16 RT outputs, each of its k rows of h a team of `team` waves that
 // split K; the rows do not wait for the experts' numbers, the weights do.
-template <int U, int Q>
+template <int RT, int U, int Q>
 __global__ __launch_bounds__(1024) void k_layer_down(const int32_t* __restrict__ ids,
                                                      const float* __restrict__ weights, int topk,
                                                      int E, int team,
@@ -240,26 +240,29 @@ __global__ __launch_bounds__(1024) void k_layer_down(const int32_t* __restrict__
                                                      const uint16_t* __restrict__ h, int N, int K,
                                                      float* __restrict__ y) {
   extern __shared__ __align__(16) unsigned char xs[];   // [topk][few_stride(K)]
-  __shared__ int amax[kTopK], tile[kTopK][16];
+  __shared__ int amax[kTopK], tile[kTopK][16 * RT];
   __shared__ float scale[kTopK], share[kTopK];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int qg = lane >> 4, r = lane & 15;
-  const int t = blockIdx.y, j = wave / team, part = wave - j * team;
+  const int t = blockIdx.y, n0 = blockIdx.x * 16 * RT;
+  const int j = wave / team, part = wave - j * team;
   const int K16 = K >> 4, nchunks = (K + 255) >> 8, stride = few_stride(K);
   const int per = (nchunks + team - 1) / team, c0 = part * per, c1 = min(c0 + per, nchunks);
-  const int n0 = blockIdx.x * 16;
-  for (int i = tid; i < kTopK * 16; i += blockDim.x) (&tile[0][0])[i] = 0;
+  for (int i = tid; i < kTopK * 16 * RT; i += blockDim.x) (&tile[0][0])[i] = 0;
   if (tid < kTopK) amax[tid] = 0;
 
   const int pair = t * topk + j;
   const void* xrow = h + (int64_t)pair * K;
   const int id = ids[pair];
   Raw4<kBf16> xr[U];
-  uint4 w[U];
+  uint4 w[RT][U];
   const bool live = id >= 0 && c0 < c1;                 // wave-uniform
   const int expert = min(max(id, 0), E - 1);
-  const uint32_t* wrow = packed + ((int64_t)expert * N + min(n0 + r, N - 1)) * K16;
+  const uint32_t* wrow[RT];
+#pragma unroll
+  for (int i = 0; i < RT; ++i)
+    wrow[i] = packed + ((int64_t)expert * N + min(n0 + 16 * i + r, N - 1)) * K16;
   if (live) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -269,8 +272,10 @@ __global__ __launch_bounds__(1024) void k_layer_down(const int32_t* __restrict__
     }
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-      w[u] = load_quad<Q>(wrow, 16 * min(c0 + u, c1 - 1) + 4 * qg, K16);
+    for (int i = 0; i < RT; ++i)
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        w[i][u] = load_quad<Q>(wrow[i], 16 * min(c0 + u, c1 - 1) + 4 * qg, K16);
   }
   const float g = gamma[expert];
   lds_sync();
@@ -315,31 +320,37 @@ __global__ __launch_bounds__(1024) void k_layer_down(const int32_t* __restrict__
     }
     sum = wave_sum_i(sum);
     wave_lds_sync();                                    // this wave's own chunks: no block barrier
-    v4i acc = {0, 0, 0, 0};
+    v4i acc[RT] = {};
     const unsigned char* xq = xs + j * stride + 64 * qg;
     for (int b0 = c0; b0 < c1; b0 += U) {
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         if (b0 + u >= c1) break;
         const uint4* xv = reinterpret_cast<const uint4*>(xq + (b0 + u) * 256);
-        const uint4 p = settle<Q>(w[u], 16 * (b0 + u) + 4 * qg, K16);
-        const uint32_t word[4] = {p.x, p.y, p.z, p.w};
-        if (b0 + U + u < c1) w[u] = load_quad<Q>(wrow, 16 * (b0 + U + u) + 4 * qg, K16);
+        uint4 b[4];
 #pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          const uint4 b = xv[v];
-          acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(
-              operand(word[v]), v4i{(int)b.x, (int)b.y, (int)b.z, (int)b.w}, acc, 0, 0, 0);
+        for (int v = 0; v < 4; ++v) b[v] = xv[v];
+#pragma unroll
+        for (int i = 0; i < RT; ++i) {
+          const uint4 p = settle<Q>(w[i][u], 16 * (b0 + u) + 4 * qg, K16);
+          const uint32_t word[4] = {p.x, p.y, p.z, p.w};
+          if (b0 + U + u < c1) w[i][u] = load_quad<Q>(wrow[i], 16 * (b0 + U + u) + 4 * qg, K16);
+#pragma unroll
+          for (int v = 0; v < 4; ++v)
+            acc[i] = __builtin_amdgcn_mfma_i32_16x16x64_i8(
+                operand(word[v]), v4i{(int)b[v].x, (int)b[v].y, (int)b[v].z, (int)b[v].w}, acc[i], 0, 0, 0);
         }
       }
     }
     if (r == 0) {
 #pragma unroll
-      for (int v = 0; v < 4; ++v) atomicAdd(&tile[j][4 * qg + v], acc[v] - sum);
+      for (int i = 0; i < RT; ++i)
+#pragma unroll
+        for (int v = 0; v < 4; ++v) atomicAdd(&tile[j][16 * i + 4 * qg + v], acc[i][v] - sum);
     }
   }
   lds_sync();
-  if (tid < 16 && n0 + tid < N) {
+  if (tid < 16 * RT && n0 + tid < N) {
     float s = 0.0f;
     for (int i = 0; i < topk; ++i)
       if (ids[t * topk + i] >= 0) s = fmaf(share[i], (float)tile[i][tid] * scale[i], s);
@@ -384,7 +395,9 @@ template <int MODE>
 hipError_t launch_gate(const LayerCall& c, const Router& rt, const void* x, const float* absmax,
                        uint16_t* h, hipStream_t stream) {
   const int64_t n = 2 * c.F;
-  const int waves = 4, bn = 16 * waves;
+  // 128 weight rows per block where that leaves blocks enough, else 64, as k_experts_few
+  // (16 tokens, 8 of 64 experts: 22.8 -> 18.1 us; one token 11.0 / 7.8)
+  const int waves = ((n + 127) / 128) * std::min(c.T * c.k, c.E) >= 512 ? 8 : 4, bn = 16 * waves;
   const dim3 grid((unsigned)((n + bn - 1) / bn), (unsigned)(c.E + 1));
   const size_t lds = rows_lds(c.K, c.T, MODE);
   auto go = [&](auto kern) {
@@ -410,10 +423,11 @@ hipError_t launch_gate(const LayerCall& c, const Router& rt, const void* x, cons
                   : by_depth(std::integral_constant<int, kWhole>{});
 }
 
+template <int RT>
 hipError_t launch_down(const LayerCall& c, const Router& rt, const uint16_t* h, hipStream_t stream) {
   const int nchunks = (int)((c.F + 255) / 256);
   const int topk = (int)c.k, team = std::max(1, std::min(16 / topk, (nchunks + 3) / 4));
-  const dim3 grid((unsigned)((c.N + 15) / 16), (unsigned)c.T);
+  const dim3 grid((unsigned)((c.N + 16 * RT - 1) / (16 * RT)), (unsigned)c.T);
   const size_t lds = (size_t)topk * few_stride((int)c.F);
   auto go = [&](auto kern) {
     hipError_t e = kern.allow_lds();
@@ -423,8 +437,18 @@ hipError_t launch_down(const LayerCall& c, const Router& rt, const uint16_t* h, 
                                                          c.gamma_down, h, (int)c.N, (int)c.F, c.y);
     return hipGetLastError();
   };
-  if (c.F < 64) return go(Kernel<k_layer_down<4, kWords>>{});
-  return c.F % 64 ? go(Kernel<k_layer_down<4, kShort>>{}) : go(Kernel<k_layer_down<4, kWhole>>{});
+  if (c.F < 64) return go(Kernel<k_layer_down<RT, 4, kWords>>{});
+  return c.F % 64 ? go(Kernel<k_layer_down<RT, 4, kShort>>{}) : go(Kernel<k_layer_down<RT, 4, kWhole>>{});
+}
+
+// 32 outputs per block where blocks of 16 would be more than four per CU, which
+// run at once (16 tokens, 8 of 64 experts, 1024 -> 2560: 18.1 -> 17.1 us; 3 tokens 6.4 / 6.6,
+// one 5.1 / 6.6; 64 outputs 19.5).  Blocks of one run of outputs side by side on an XCD,
+// for its L2, gained nothing (19.7).
+hipError_t launch_down_by_size(const LayerCall& c, const Router& rt, const uint16_t* h,
+                               hipStream_t stream) {
+  return (c.N + 15) / 16 * c.T > 4 * device_cus() ? launch_down<2>(c, rt, h, stream)
+                                                  : launch_down<1>(c, rt, h, stream);
 }
 
 bool two_launches(const LayerCall& c) {
@@ -462,7 +486,7 @@ hipError_t launch_layer(const LayerCall& c, hipStream_t stream) {
         if (e == hipSuccess) e = launch_gate<kInt8>(c, rt, xq, f32(l.absmax), h, stream);
       }
     }
-    return e == hipSuccess ? launch_down(c, rt, h, stream) : e;
+    return e == hipSuccess ? launch_down_by_size(c, rt, h, stream) : e;
   }
   // the three calls, one after the other
   const bl_routing r{c.T, c.k, c.E, i32(l.offsets), i32(l.pairs), i32(l.slots), f32(l.weights)};
