@@ -21,6 +21,7 @@ namespace {
 
 constexpr int kTokens = 16;        // most tokens of the two launches: the columns of an MFMA
 constexpr int kRawTokens = 4;      // most whose step A1 every block repeats
+constexpr int kPairTokens = 4;     // most whose blocks belong to (token, rank) pairs
 constexpr int kTopK = 16;          // most experts per token: one DPP row
 constexpr int kLayerExperts = 256; // most experts: 16 logits per lane of a row
 
@@ -90,9 +91,67 @@ __device__ __forceinline__ void choose_rows(const Router& r) {
   }
 }
 
-// Gate and up projections (as k_experts_few): block (row tile, 1 + expert), and
-// the block (0, 0) that chooses.  N rows of gate and up together; h by token * k + rank.
-template <int MODE, int U, int Q>
+// Keys of a token's logits, 64 v + lane in key[v].
+struct Keys {
+  uint32_t key[kLayerExperts / 64];
+  __device__ __forceinline__ Keys(const Router& r, int t) {
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int v = 0; v < kLayerExperts / 64; ++v) {
+      const int e = v * 64 + lane;
+      key[v] = e < r.E ? logit_key(r, (int64_t)t * r.E + e) : 0;
+    }
+  }
+  __device__ __forceinline__ uint32_t of(int e) const {
+    uint32_t k = 0;
+#pragma unroll
+    for (int v = 0; v < kLayerExperts / 64; ++v)
+      if (e >> 6 == v) k = __builtin_amdgcn_readlane(key[v], e & 63);
+    return k;
+  }
+};
+
+// The expert of a token's rank j, -1 if fewer logits are usable, by a block of four
+// waves: each counts for every key what comes before it among 16 of every 64 keys.
+__device__ __forceinline__ int expert_of_rank(const Keys& a, int E, int j, int wave,
+                                              int (*part)[kLayerExperts]) {
+  constexpr int V = kLayerExperts / 64;
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    if (v * 64 >= E) break;
+    int before = 0;
+#pragma unroll
+    for (int w = 0; w < V; ++w) {
+      if (w * 64 >= E) break;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const int l = wave * 16 + i;
+        const uint32_t other = __builtin_amdgcn_readlane(a.key[w], l);
+        // equal keys: the lower expert first (key 0, unusable, is not asked for)
+        before += other > a.key[v] - (w < v || (w == v && l < lane) ? 1u : 0u);
+      }
+    }
+    part[wave][v * 64 + lane] = before;
+  }
+  lds_sync();
+  int expert = -1;
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    if (v * 64 >= E) break;
+    const int e = v * 64 + lane, before = part[0][e] + part[1][e] + part[2][e] + part[3][e];
+    const uint64_t here = __ballot(a.key[v] && before == j);
+    if (here) expert = v * 64 + __builtin_ctzll(here);
+  }
+  return expert;
+}
+
+// Gate and up projections (as k_experts_few): block (row tile, 1 + expert) or, PAIRS,
+// (row tile, 1 + token * k + rank), and the block (0, 0) that chooses.  Most blocks of an
+// expert have nothing to do while few tokens meet many experts; a block of a pair
+// first finds its expert, and ends if an earlier token takes the same one.
+// N rows of gate and up together; h by token * k + rank.
+template <int MODE, bool PAIRS, int U, int Q>
 __global__ __launch_bounds__(512) void k_layer_gate(const Router rt,
                                                     const uint32_t* __restrict__ packed,
                                                     const float* __restrict__ gamma_gate,
@@ -106,27 +165,46 @@ __global__ __launch_bounds__(512) void k_layer_gate(const Router rt,
     if (blockIdx.x == 0) choose_rows(rt);
     return;
   }
-  const int expert = blockIdx.y - 1;
   const int tid = threadIdx.x, lane = tid & 63, nthreads = blockDim.x;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), nwaves = nthreads >> 6;
   const int qg = lane >> 4, r = lane & 15;
 
-  // ranks of this expert: -1 where a token does not take it
+  // ranks of the block's expert: -1 where a token does not take it
   if (tid < kTokens) {
     rank[tid] = -1;
     qsum[tid] = amax[tid] = 0;
   }
-  lds_sync();
-  for (int t = wave; t < rt.T; t += nwaves) {
-    const int64_t row = (int64_t)t * rt.E;
-    const uint32_t own = logit_key(rt, row + expert);
-    int before = 0;
-    for (int e = lane; e < rt.E; e += 64) {
-      const uint32_t key = logit_key(rt, row + e);
-      before += key > own || (key == own && e < expert);
-    }
+  int expert = blockIdx.y - 1;
+  auto keep = [&](int t, uint32_t own, int before) {
     before = wave_sum_i(before);
     if (lane == 0 && own && before < rt.k) rank[t] = before;
+  };
+  if constexpr (PAIRS) {
+    __shared__ int part[4][kLayerExperts];
+    const int t0 = expert / rt.k, j = expert - t0 * rt.k;
+    const Keys a(rt, t0), b(rt, min(wave, rt.T - 1));
+    expert = expert_of_rank(a, rt.E, j, wave, part);
+    if (expert < 0) return;
+    for (int t = wave; t < rt.T; t += 4) {
+      const uint32_t own = b.of(expert);
+      int before = 0;
+#pragma unroll
+      for (int v = 0; v < kLayerExperts / 64; ++v)
+        before += b.key[v] > own || (b.key[v] == own && v * 64 + lane < expert);
+      keep(t, own, before);
+    }
+  } else {
+    lds_sync();
+    for (int t = wave; t < rt.T; t += nwaves) {
+      const int64_t row = (int64_t)t * rt.E;
+      const uint32_t own = logit_key(rt, row + expert);
+      int before = 0;
+      for (int e = lane; e < rt.E; e += 64) {
+        const uint32_t key = logit_key(rt, row + e);
+        before += key > own || (key == own && e < expert);
+      }
+      keep(t, own, before);
+    }
   }
   lds_sync();
   const int my_rank = rank[r];
@@ -135,6 +213,7 @@ __global__ __launch_bounds__(512) void k_layer_gate(const Router rt,
   if (nrow == 0) return;
   // lane r's token: the r-th member (the first in place of those that are missing)
   int token = __builtin_ctz(members);
+  if (PAIRS && token != (int)(blockIdx.y - 1) / rt.k) return;   // an earlier token's block does it
   {
     uint32_t m = members;
     for (int i = 0; i < 16; ++i) {
@@ -391,14 +470,15 @@ size_t rows_lds(int64_t k, int64_t rows, int mode) {
   return (size_t)rows * (few_stride((int)k) + (mode == kInt8 ? 0 : mode == kBf16 ? 2 * k : 4 * k));
 }
 
-template <int MODE>
+template <int MODE, bool PAIRS>
 hipError_t launch_gate(const LayerCall& c, const Router& rt, const void* x, const float* absmax,
                        uint16_t* h, hipStream_t stream) {
   const int64_t n = 2 * c.F;
   // 128 weight rows per block where that leaves blocks enough, else 64, as k_experts_few
   // (16 tokens, 8 of 64 experts: 22.8 -> 18.1 us; one token 11.0 / 7.8)
-  const int waves = ((n + 127) / 128) * std::min(c.T * c.k, c.E) >= 512 ? 8 : 4, bn = 16 * waves;
-  const dim3 grid((unsigned)((n + bn - 1) / bn), (unsigned)(c.E + 1));
+  const int waves = !PAIRS && ((n + 127) / 128) * std::min(c.T * c.k, c.E) >= 512 ? 8 : 4,
+            bn = 16 * waves;
+  const dim3 grid((unsigned)((n + bn - 1) / bn), (unsigned)((PAIRS ? c.T * c.k : c.E) + 1));
   const size_t lds = rows_lds(c.K, c.T, MODE);
   auto go = [&](auto kern) {
     hipError_t e = kern.allow_lds();
@@ -408,19 +488,31 @@ hipError_t launch_gate(const LayerCall& c, const Router& rt, const void* x, cons
                                                    (int)c.K, h);
     return hipGetLastError();
   };
-  if (c.K < 64) return go(Kernel<k_layer_gate<MODE, 2, kWords>>{});
+  if (c.K < 64) return go(Kernel<k_layer_gate<MODE, PAIRS, 2, kWords>>{});
   auto by_depth = [&](auto quads) {
     constexpr int Q = decltype(quads)::value;
     switch (few_depth(c.K)) {
-      case 2: return go(Kernel<k_layer_gate<MODE, 2, Q>>{});
-      case 4: return go(Kernel<k_layer_gate<MODE, 4, Q>>{});
-      case 6: return go(Kernel<k_layer_gate<MODE, 6, Q>>{});
-      case 8: return go(Kernel<k_layer_gate<MODE, 8, Q>>{});
-      default: return go(Kernel<k_layer_gate<MODE, 10, Q>>{});
+      case 2: return go(Kernel<k_layer_gate<MODE, PAIRS, 2, Q>>{});
+      case 4: return go(Kernel<k_layer_gate<MODE, PAIRS, 4, Q>>{});
+      case 6: return go(Kernel<k_layer_gate<MODE, PAIRS, 6, Q>>{});
+      case 8: return go(Kernel<k_layer_gate<MODE, PAIRS, 8, Q>>{});
+      default: return go(Kernel<k_layer_gate<MODE, PAIRS, 10, Q>>{});
     }
   };
   return c.K % 64 ? by_depth(std::integral_constant<int, kShort>{})
                   : by_depth(std::integral_constant<int, kWhole>{});
+}
+
+// Blocks of (token, rank) pairs for at most four tokens, whose waves rank a token each,
+// where at most half as many as blocks of experts.  Per expert / per pair: one
+// token, 8 of 64 experts 10.4 / 8.7 us, of 128 10.7 / 8.4, of 256 13.1 / 11.3; four tokens,
+// 8 of 64 13.8 / 12.0; but one token, 8 of 16 7.6 / 8.2, 4 of 32 7.3 / 7.7.
+template <int MODE>
+hipError_t launch_gate(const LayerCall& c, const Router& rt, const void* x, const float* absmax,
+                       uint16_t* h, hipStream_t stream) {
+  const bool pairs = c.T <= kPairTokens && c.E >= 64 && 2 * c.T * c.k <= c.E;
+  return pairs ? launch_gate<MODE, true>(c, rt, x, absmax, h, stream)
+               : launch_gate<MODE, false>(c, rt, x, absmax, h, stream);
 }
 
 template <int RT>

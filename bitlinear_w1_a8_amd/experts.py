@@ -7,6 +7,7 @@ the caller's device and every step runs in the library's HIP kernels on the
 current stream of that device.
 """
 
+import functools
 import operator
 import struct
 
@@ -218,6 +219,12 @@ def linear_experts(x, packed, gamma, routing, combine=True, x_rows="slots", want
     return (y, acc) if want_acc else y
 
 
+@functools.lru_cache(maxsize=256)
+def _ffn_workspace(*sizes):
+    """The library's answer, which depends on these sizes alone."""
+    return _load().bitlinear_experts_ffn_workspace_bytes(*sizes)
+
+
 def experts_ffn(x, logits, k, packed_gu, gamma_gate, gamma_up, packed_down, gamma_down, absmax=None,
                 share="chosen", out=None):
     """A whole routed layer, the same bits as route_experts, gated_relu2_experts
@@ -266,7 +273,7 @@ def experts_ffn(x, logits, k, packed_gu, gamma_gate, gamma_up, packed_down, gamm
         need(dev, absmax, "absmax", torch.float32, (t,))
     on = x.device
     y = _out(dev, out, (t, n), torch.float32, on)
-    wsb = lib.bitlinear_experts_ffn_workspace_bytes(t, e, k, f, kk, n)
+    wsb = _ffn_workspace(t, e, k, f, kk, n)
     ws = torch.empty(wsb, dtype=torch.uint8, device=on)
     call(dev, lib.bitlinear_experts_ffn, logits.data_ptr(), lt, t, e, k, SHARES[share], x.data_ptr(),
          dt, None if absmax is None else absmax.data_ptr(), packed_gu.data_ptr(),

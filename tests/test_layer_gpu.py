@@ -102,6 +102,25 @@ def test_masks_and_ties(bl, t):
     assert (t == 4 or t > 1 and none.any()) and torch.all(got[none] == 0) or t == 1
 
 
+@pytest.mark.parametrize("t,e,k", [(1, 64, 8), (2, 64, 16), (3, 64, 6), (4, 64, 8), (4, 100, 12), (1, 128, 1),
+                                   (4, 129, 16), (3, 192, 5), (4, 256, 16), (1, 255, 16), (2, 256, 3)])
+def test_few_tokens_of_many_experts(bl, t, e, k):
+    """Ties across a wave's 64 logits, experts that several tokens take at different
+    ranks, tokens with fewer usable logits than k or none."""
+    layer = Layer(bl, e, 96, 272, 50)
+    x, logits = _tokens(t, 272, e)
+    same = logits[:1].expand(t, e).contiguous()
+    few = torch.full_like(logits, float("-inf"))
+    few[0, e - 1] = few[t // 2, e // 2] = float("inf")
+    few[t - 1, 3 % e] = -3.4028234663852886e38
+    mixed = logits.clone()
+    mixed[t - 1] = float("nan")
+    shifted = torch.stack([logits[0].roll(i) + 0.01 * i for i in range(t)])
+    for l in (logits.round(), torch.zeros_like(logits), same, few, mixed, shifted, -logits.abs().round()):
+        _check(bl, layer, x, l, k)
+        _check(bl, layer, x, l.bfloat16(), k, "all")
+
+
 def test_everything_masked_and_one_expert_takes_all(bl):
     layer = Layer(bl, 32, 64, 128, 40)
     x, logits = _tokens(16, 128, 32)
