@@ -317,7 +317,7 @@ using S2 = std::integral_constant<int, 2>;
 // every GROUPS-th block of K through buffers of its own, and their sums meet at the end.
 //   4 x 2 waves, one group, three buffers: tiles of 256 x 128, where there are enough
 //   2 x 2 waves, two groups, two buffers:  tiles of 128 x 128, where there are not: twice
-//     the waves on a CU (128 x 2560 x 6912 62 -> ?? us)
+//     the waves on a CU (20 tiles of K = 6912: 62 -> 48 us)
 // NATIVE: e4m3 instructions; else each wave widens its operands to f16.
 template <bool BF16, bool NATIVE, bool TAIL, int WR, int WT, int GROUPS, int STAGES>
 __global__ __launch_bounds__(64 * WR * WT * GROUPS) void k_f8_tile(

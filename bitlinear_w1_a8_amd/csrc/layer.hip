@@ -20,7 +20,7 @@ namespace bl {
 namespace {
 
 constexpr int kTokens = 16;        // most tokens of the two launches: the columns of an MFMA
-constexpr int kRawTokens = 4;      // most whose step A1 every block repeats
+constexpr int kRawTokens = 6;      // most whose step A1 every block repeats
 constexpr int kPairTokens = 4;     // most whose blocks belong to (token, rank) pairs
 constexpr int kTopK = 16;          // most experts per token: one DPP row
 constexpr int kLayerExperts = 256; // most experts: 16 logits per lane of a row
@@ -151,6 +151,9 @@ __device__ __forceinline__ int expert_of_rank(const Keys& a, int E, int j, int w
 // expert have nothing to do while few tokens meet many experts; a block of a pair
 // first finds its expert, and ends if an earlier token takes the same one.
 // N rows of gate and up together; h by token * k + rank.
+// Bound by the start of its blocks and two loads one after the other (logits, then
+// weights: one token, 8 of 64 experts of 2560 -> 2 x 1024, 10.5 MB in 8.7 us), with
+// many experts by the stream of weights (16 tokens, 8 of 64, 75 MB in 18 us, 4.1 TB/s).
 template <int MODE, bool PAIRS, int U, int Q>
 __global__ __launch_bounds__(512) void k_layer_gate(const Router rt,
                                                     const uint32_t* __restrict__ packed,
@@ -310,6 +313,9 @@ __global__ __launch_bounds__(512) void k_layer_gate(const Router rt,
 // Down projections and the weighted sum (as k_experts_token): a block has one
 // token and 16 RT outputs, each of its k rows of h a team of `team` waves that
 // split K; the rows do not wait for the experts' numbers, the weights do.
+// (One token, 8 experts of 1024 -> 2560, 5.2 MB in 5.1 us: the latency of the number, the
+// weights and three barriers; 16 tokens 17 us, each expert's weights once per token
+// from the caches, 84 MB at 4.9 TB/s.)
 template <int RT, int U, int Q>
 __global__ __launch_bounds__(1024) void k_layer_down(const int32_t* __restrict__ ids,
                                                      const float* __restrict__ weights, int topk,
@@ -543,6 +549,15 @@ hipError_t launch_down_by_size(const LayerCall& c, const Router& rt, const uint1
                                                   : launch_down<1>(c, rt, h, stream);
 }
 
+// Step A1 in every block, or in a launch of its own before.  Its own / in the blocks,
+// bfloat16, 8 of 64 experts of 2560 -> 1024 -> 2560: one token 16.2 / 13.9 us, four 22.4 /
+// 20.8, six 27.3 / 26.6, eight 29.5 / 30.4, sixteen 39.1 / 47.0; 2 of 16 of 4096, six 36.4 / 32.3,
+// eight 41.8 / 43.1.  Rows of binary32 take LDS from other blocks: three tokens of 2560
+// (38 KB) 20.1 / 19.3, four (51 KB) 22.5 / 25.6, of 4096 three (61 KB) 26.3 / 28.1.
+bool in_blocks(const LayerCall& c, int mode) {
+  return c.T <= kRawTokens && rows_lds(c.K, c.T, mode) <= (size_t)(mode == kBf16 ? kMaxLds : 48 * 1024);
+}
+
 bool two_launches(const LayerCall& c) {
   // the last: blocks of up to 1024 threads, fewer than 2^32 of them in a row of the grid
   return c.T <= kTokens && c.k <= kTopK && c.E <= kLayerExperts &&
@@ -570,7 +585,7 @@ hipError_t launch_layer(const LayerCall& c, hipStream_t stream) {
       e = launch_gate<kInt8>(c, rt, c.x, c.absmax, h, stream);
     } else {
       const int mode = c.x_dtype == BL_BF16 ? kBf16 : kF32;
-      if (c.T <= kRawTokens && rows_lds(c.K, c.T, mode) <= (size_t)kMaxLds) {
+      if (in_blocks(c, mode)) {
         e = mode == kBf16 ? launch_gate<kBf16>(c, rt, c.x, nullptr, h, stream)
                           : launch_gate<kF32>(c, rt, c.x, nullptr, h, stream);
       } else {

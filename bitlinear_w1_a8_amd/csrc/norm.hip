@@ -3,9 +3,10 @@
 // 128), in one pass over memory.
 //
 // A block has one token and keeps the row in registers as u = total * g, eight
-// consecutive elements per vector, VPT vectors per thread (what a longer row
+// consecutive elements per vector, two vectors per thread (what a longer row
 // has beyond them is computed again from `total`, which each thread has itself
-// written).  One exchange between the waves gives the sum of squares and
+// written; one, two and four vectors are alike: 4096 x 2560 21.4 / 21.7 / 21.8 us, 1000
+// x 28672 59.4 / 56.8 / 60.6, one token of 8192 4.0 / 3.6 / 4.3).  One exchange between the waves gives the sum of squares and
 // the largest |u|; rounding is monotonic, so max |x_hat| = RN32(max |u| * r)
 // and no second exchange is needed (a group of 128 is one DPP row of 16 lanes).
 //
@@ -18,6 +19,11 @@
 // product with 1 / K and of the ends themselves) round to the same binary32,
 // that is ms; all steps from S to ms are monotonic.  Else, about one row in
 // 2^19, the row is summed again exactly, in buckets by exponent.
+//
+// Bound by memory (binary32 x, bfloat16 residual, int8 codes, 9 bytes an element:
+// 4096 x 2560 21.5 us, 4.4 TB/s; 1000 x 28672 56.8 us, 4.5; a large copy reaches 4.7), for
+// few tokens by the latency of a launch, a load, the exchange and a store
+// (one token of 2560 3.2 us).
 #include <algorithm>
 #include <type_traits>
 
@@ -67,7 +73,9 @@ struct Args {
   int64_t T, row0;                 // all tokens; the first of this launch
 };
 
-template <bool XBF16, int RES, bool F8, int VPT>
+constexpr int kVectors = 2;             // vectors per thread
+
+template <bool XBF16, int RES, bool F8>
 __global__ __launch_bounds__(1024) void k_add_subln(const Args a) {
   __shared__ double red_s[kMaxWaves];
   __shared__ int red_m[kMaxWaves], red_q[kMaxWaves];
@@ -125,14 +133,14 @@ __global__ __launch_bounds__(1024) void k_add_subln(const Args a) {
     f[4] *= g1.x; f[5] *= g1.y; f[6] *= g1.z; f[7] *= g1.w;
   };
 
-  float u[VPT][8];
+  float u[kVectors][8];
   double sq = 0.0;
   int most = 0;
   {
-    Vec8<XBF16> x[VPT];
-    Vec8<RBF16> r[VPT];
+    Vec8<XBF16> x[kVectors];
+    Vec8<RBF16> r[kVectors];
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) {
+    for (int i = 0; i < kVectors; ++i) {
       const int v = tid + i * nthr;
       if (v < nvec) {
         x[i].load(xr, 8 * v);
@@ -140,7 +148,7 @@ __global__ __launch_bounds__(1024) void k_add_subln(const Args a) {
       }
     }
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) {
+    for (int i = 0; i < kVectors; ++i) {
       const int v = tid + i * nthr;
 #pragma unroll
       for (int e = 0; e < 8; ++e) u[i][e] = 0.0f;
@@ -156,7 +164,7 @@ __global__ __launch_bounds__(1024) void k_add_subln(const Args a) {
       }
     }
   }
-  for (int v = tid + VPT * nthr; v < nvec; v += nthr) {
+  for (int v = tid + kVectors * nthr; v < nvec; v += nthr) {
     Vec8<XBF16> x;
     Vec8<RBF16> r;
     float f[8];
@@ -236,8 +244,8 @@ __global__ __launch_bounds__(1024) void k_add_subln(const Args a) {
       }
     };
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) put(tid + i * nthr, u[i]);
-    for (int v0 = VPT * nthr; v0 < nvec; v0 += nthr) {   // whole waves go round
+    for (int i = 0; i < kVectors; ++i) put(tid + i * nthr, u[i]);
+    for (int v0 = kVectors * nthr; v0 < nvec; v0 += nthr) {   // whole waves go round
       const int v = v0 + tid;
       float f[8] = {};
       if (v < nvec) {
@@ -265,9 +273,9 @@ __global__ __launch_bounds__(1024) void k_add_subln(const Args a) {
       *reinterpret_cast<uint2*>(qr + 8 * v) = make_uint2(w[0], w[1]);
     };
 #pragma unroll
-    for (int i = 0; i < VPT; ++i)
+    for (int i = 0; i < kVectors; ++i)
       if (tid + i * nthr < nvec) put(tid + i * nthr, u[i]);
-    for (int v = tid + VPT * nthr; v < nvec; v += nthr) {
+    for (int v = tid + kVectors * nthr; v < nvec; v += nthr) {
       float f[8];
       again(8 * v, f);
       times_gain(8 * v, f);
@@ -292,16 +300,13 @@ hipError_t launch(const Args& base, int64_t t, hipStream_t stream) {
   const int64_t nvec = base.K / 8;
   // a launch has fewer than 2^32 threads, and a row takes up to 1024 of them
   constexpr int64_t kMost = int64_t(1) << 21;
-  int vpt = 2;
-  while (vpt < 4 && nvec > vpt * 1024) vpt *= 2;
-  const int64_t thr = std::min<int64_t>(1024, ((nvec + vpt - 1) / vpt + 63) / 64 * 64);
+  const int64_t thr = std::min<int64_t>(1024, ((nvec + kVectors - 1) / kVectors + 63) / 64 * 64);
   hipError_t e = hipSuccess;
   for (int64_t r = 0; e == hipSuccess && r < t; r += kMost) {
     Args a = base;
     a.row0 = r;
     const dim3 grid((unsigned)std::min(t - r, kMost)), block((unsigned)thr);
-    if (vpt == 2) k_add_subln<XBF16, RES, F8, 2><<<grid, block, 0, stream>>>(a);
-    else k_add_subln<XBF16, RES, F8, 4><<<grid, block, 0, stream>>>(a);
+    k_add_subln<XBF16, RES, F8><<<grid, block, 0, stream>>>(a);
     e = hipGetLastError();
   }
   return e;
