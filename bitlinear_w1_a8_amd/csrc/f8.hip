@@ -118,7 +118,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_f8_few(const uint8_t* __rest
   };
   auto load = [&](Buf& f, int kb) {
     kb = min(kb, kb_all - 1);
-    const int k0 = min(kb * kF8Block + 32 * g, K - 16), k1 = min(kb * kF8Block + 32 * g + 16, K - 16);
+    const int k0 = min(kb * kF8Block + 16 * g, K - 16), k1 = min(kb * kF8Block + 64 + 16 * g, K - 16);
 #pragma unroll
     for (int i = 0; i < RT; ++i) {
       f.a[i][0] = *reinterpret_cast<const uint4*>(wrow[i] + k0);
@@ -148,11 +148,11 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_f8_few(const uint8_t* __rest
       Buf f = buf[u];
       if (kb + U * WV < kb_all) load(buf[u], kb + U * WV);
       if ((kb + 1) * kF8Block > K) {           // tokens are zero past K
-        const int k = kb * kF8Block + 32 * g;
+        const int k = kb * kF8Block + 16 * g;
 #pragma unroll
         for (int j = 0; j < TT; ++j) {
           if (k >= K) f.b[j][0] = make_uint4(0, 0, 0, 0);
-          if (k + 16 >= K) f.b[j][1] = make_uint4(0, 0, 0, 0);
+          if (k + 64 >= K) f.b[j][1] = make_uint4(0, 0, 0, 0);
         }
       }
       v4f p[RT][TT];
@@ -314,10 +314,12 @@ using S1 = std::integral_constant<int, 1>;
 using S2 = std::integral_constant<int, 2>;
 
 // WR x WT waves of 64 rows x 64 tokens each, GROUPS times: each group takes
-// every GROUPS-th block of K through buffers of its own, and their sums meet at the end.
-//   4 x 2 waves, one group, three buffers: tiles of 256 x 128, where there are enough
-//   2 x 2 waves, two groups, two buffers:  tiles of 128 x 128, where there are not: twice
-//     the waves on a CU (20 tiles of K = 6912: 62 -> 48 us)
+// every GROUPS-th block of K through buffers of its own, and their sums meet at the end, in
+// order.  A wave takes about a microsecond per block of K, most of it issue, so where there
+// are few tiles the CU's other SIMDs take other blocks of K; LDS holds what is on its way.
+// (6912 -> 2560, 256 tokens, binary32 outputs: 64 x 64 in two groups with three buffers 27.1 us,
+// in four with two 24.6, in three with three 22.4; 128 x 64 in two with three 32.7; 128 x 128 in
+// two with two 50.)
 // NATIVE: e4m3 instructions; else each wave widens its operands to f16.
 template <bool BF16, bool NATIVE, bool TAIL, int WR, int WT, int GROUPS, int STAGES>
 __global__ __launch_bounds__(64 * WR * WT * GROUPS) void k_f8_tile(
@@ -449,8 +451,9 @@ __global__ __launch_bounds__(64 * WR * WT * GROUPS) void k_f8_tile(
   if constexpr (STAGES == 3)
     if (at + 1 < steps) step(S1{}, at + 1);
   wait_vmem<0>();                                   // loads past the end land before LDS is used anew
-  if constexpr (GROUPS == 2) {
-    static_assert(GROUPS * kA >= 2 * 16 * 4 * 64 * kWaves, "half of a group's sums in one buffer");
+  if constexpr (GROUPS > 1) {
+    constexpr int kSums = 2 * 16 * 64 * kWaves;     // half of a group's sums
+    static_assert(GROUPS * kA >= (GROUPS - 1) * kSums * 4, "half of the groups' sums in one buffer");
     lds_sync();
     float* part[2] = {reinterpret_cast<float*>(a0), reinterpret_cast<float*>(a1)};
     const int me = wave * 64 + lane;
@@ -460,15 +463,17 @@ __global__ __launch_bounds__(64 * WR * WT * GROUPS) void k_f8_tile(
       for (int j = 0; j < 2; ++j)
 #pragma unroll
         for (int v = 0; v < 16; ++v)
-          if (group) part[i][(j * 16 + v) * 64 * kWaves + me] = acc[i][j][v];
+          if (group) part[i][(group - 1) * kSums + (j * 16 + v) * 64 * kWaves + me] = acc[i][j][v];
     lds_sync();
     if (group) return;
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int g = 0; g < GROUPS - 1; ++g)            // in order of the groups
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
+      for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int v = 0; v < 16; ++v) acc[i][j][v] += part[i][(j * 16 + v) * 64 * kWaves + me];
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int v = 0; v < 16; ++v) acc[i][j][v] += part[i][g * kSums + (j * 16 + v) * 64 * kWaves + me];
   }
 #pragma unroll
   for (int i = 0; i < 2; ++i)
@@ -657,7 +662,7 @@ __global__ __launch_bounds__(256) void k_unpack_f8(const uint32_t* __restrict__ 
   }
 }
 
-// T * N <= 2^36: fewer than 2^23 tiles of 128 x 128, 2^32 threads.
+// T * N <= 2^36: about 2^24 tiles of 64 x 64 at most, of 192 threads, fewer than 2^32.
 template <int BM, int BT, typename F>
 hipError_t launch_tiles(F whole, F tail, int threads, const uint8_t* w, const float* ws, const uint8_t* xq,
                         const float* xs, int64_t t, int64_t n, int64_t k, void* y, hipStream_t stream) {
@@ -667,10 +672,18 @@ hipError_t launch_tiles(F whole, F tail, int threads, const uint8_t* w, const fl
   return hipGetLastError();
 }
 
+template <bool BF16, int WR, int WT, int GROUPS, int STAGES>
+hipError_t launch_tile(const uint8_t* w, const float* ws, const uint8_t* xq, const float* xs, int64_t t,
+                       int64_t n, int64_t k, void* y, hipStream_t stream) {
+  return launch_tiles<64 * WR, 64 * WT>(k_f8_tile<BF16, BF16, false, WR, WT, GROUPS, STAGES>,
+                                        k_f8_tile<BF16, BF16, true, WR, WT, GROUPS, STAGES>,
+                                        64 * WR * WT * GROUPS, w, ws, xq, xs, t, n, k, y, stream);
+}
+
 template <bool BF16>
 hipError_t forward(const uint8_t* w, const float* ws, const uint8_t* xq, const float* xs, int64_t t,
                    int64_t n, int64_t k, void* y, hipStream_t stream) {
-  const F8Kernel kernel = f8_kernel(t, n, BF16, device_cus());
+  const F8Kernel kernel = f8_kernel(t, n, k, BF16, device_cus());
   switch (kernel) {
     case kF8Few1:
     case kF8Few2: {
@@ -678,19 +691,19 @@ hipError_t forward(const uint8_t* w, const float* ws, const uint8_t* xq, const f
       // fewer than 2^32 threads: many tokens come here with few rows only
       const int t_tiles = (int)((t + 63) / 64);
       const unsigned grid = (unsigned)((n + rows - 1) / rows * t_tiles);
-      auto* f = rows == 16 ? (t <= 16 ? k_f8_few<1, 1, BF16> : t <= 32 ? k_f8_few<2, 1, BF16> : k_f8_few<4, 1, BF16>)
-                           : (t <= 32 ? k_f8_few<2, 2, BF16> : k_f8_few<4, 2, BF16>);
+      auto* f = rows == 32 ? k_f8_few<2, 2, BF16>
+              : t <= 16    ? k_f8_few<1, 1, BF16>
+              : t <= 32    ? k_f8_few<2, 1, BF16>
+                           : k_f8_few<4, 1, BF16>;
       f<<<grid, 64 * kFewWaves, 0, stream>>>(w, ws, xq, xs, (int)t, (int)n, (int)k, t_tiles, y);
       return hipGetLastError();
     }
     case kF8Turns:
       return launch_tiles<256, 256>(k_f8_turns<false>, k_f8_turns<true>, 512, w, ws, xq, xs, t, n, k, y, stream);
-    case kF8Wide:
-      return launch_tiles<256, 128>(k_f8_tile<BF16, BF16, false, 4, 2, 1, 3>, k_f8_tile<BF16, BF16, true, 4, 2, 1, 3>,
-                                    512, w, ws, xq, xs, t, n, k, y, stream);
-    default:
-      return launch_tiles<128, 128>(k_f8_tile<BF16, BF16, false, 2, 2, 2, 2>, k_f8_tile<BF16, BF16, true, 2, 2, 2, 2>,
-                                    512, w, ws, xq, xs, t, n, k, y, stream);
+    case kF8Wide: return launch_tile<BF16, 4, 2, 1, 3>(w, ws, xq, xs, t, n, k, y, stream);
+    case kF8Square: return launch_tile<BF16, 2, 2, 2, 2>(w, ws, xq, xs, t, n, k, y, stream);
+    case kF8Tall: return launch_tile<BF16, 2, 1, 2, 3>(w, ws, xq, xs, t, n, k, y, stream);
+    default: return launch_tile<BF16, 1, 1, 3, 3>(w, ws, xq, xs, t, n, k, y, stream);
   }
 }
 

@@ -4,47 +4,66 @@
 
 #include <stdint.h>
 
-#include <algorithm>
-
 namespace bl {
 
 enum F8Kernel {
   kF8Few1,     // k_f8_few, 16 rows per block
-  kF8Few2,     // k_f8_few, 32 rows per block
-  kF8Split,    // k_f8_tile, 128 x 128, two groups of waves that share K
+  kF8Few2,     // k_f8_few, 32 rows per block (17 to 32 tokens)
+  kF8Small,    // k_f8_tile, 64 x 64, three groups of waves that share K
+  kF8Tall,     // k_f8_tile, 128 x 64, two groups
+  kF8Square,   // k_f8_tile, 128 x 128, two groups
   kF8Wide,     // k_f8_tile, 256 x 128
   kF8Turns,    // k_f8_turns, 256 x 256 (bfloat16 outputs only)
 };
 
-// Up to 32 tokens the streaming kernel, beyond them the least of these estimates
-// of the time per block of 128 k, in microseconds, from cases on 256 CUs with weights
-// from memory: a kernel of tiles takes its time per round of one tile per CU,
-// the streaming kernel grows with rows and tokens.  Streaming / 128 x 128 / 256 x 128 /
-// 256 x 256, binary32 and bfloat16 outputs:
-//    96 tokens, 2560 -> 2560    11.0 / 22.5 / 36.0       10.5 / 15.9 / 22.5 / 28.9 us
-//    96 tokens, 2560 -> 6912    18.4 / 22.8 / 36.6       18.0 / 16.2 / 23.1 / 29.3
-//   256 tokens, 2560 -> 6912    38.1 / 24.3 / 39.3       36.9 / 17.5 / 24.4 / 36.4
-//   250 tokens, 8192 -> 28672    347 / 145 / 127          344 / 111 / 82 / 127
-//   256 tokens, 28672 -> 8192    317 / 221 / 322          316 / 183 / 216 / 382
-//  1024 tokens, 2560 -> 6912     129 / 56.0 / 44.5        125 / 39.7 / 28.4 / 42.6
-//  2048 tokens, 6912 -> 2560     216 / 109 / 87.9         213 / 77.7 / 56.5 / 102
-//  2048 tokens, 2560 -> 6912     248 / 108 / 87.9         242 / 79.0 / 57.8 / 51.8
-//  4096 tokens, 2560 -> 6912     493 / 203 / 175          480 / 155 / 112 / 102
-// 16 rows per block where blocks of 32 would leave half the CUs idle, and up to 16
-// tokens always (13 tokens, 6912 -> 2560 8.3 against 11.7 us; 4 tokens, 8192 -> 28672
-// 43.1 / 48.7; 32 tokens 12.4 / 16.2 and 80.8 / 72.2; 64 tokens, 2560 -> 6912 16.5 / 11.0).
-inline F8Kernel f8_kernel(int64_t t, int64_t n, bool bf16, int cus) {
-  const F8Kernel few = t <= 16 || (n + 31) / 32 < cus / 2 ? kF8Few1 : kF8Few2;
-  if (t <= 32) return few;
-  auto rounds = [&](int64_t rows, int64_t tokens) {
-    const int64_t tiles = ((n + rows - 1) / rows) * ((t + tokens - 1) / tokens);
-    return (double)((tiles + cus - 1) / cus);
+// Up to 16 tokens the streaming kernel, beyond them the least of these estimates, in
+// microseconds.  A kernel of tiles takes rounds of one tile per CU, each of them a
+// time per block of 128 k and one for its start and end; the streaming kernel grows
+// with rows and lots of 64 tokens.  Fitted to graph replays of every kernel at 138
+// sizes (8 to 2048 tokens) with weights from memory; what the rule takes was 0.8%
+// behind the fastest on average, 15% at most.  Some of them, streaming / 64 x 64 / 128 x
+// 64 / 128 x 128 / 256 x 128 / 256 x 256:
+//   binary32 outputs
+//    32 tokens, 2560 -> 6912      8.1 / 11.4 / 15.0 / 20.3 / 32.4
+//    96 tokens, 6912 -> 2560     36.2 / 22.0 / 32.6 / 48.3 / 82.5
+//   128 tokens, 5136 -> 13942    60.8 / 41.9 / 33.4 / 48.5 / 72.0
+//   256 tokens, 8192 -> 28672     353 / 181 / 159 / 143 / 125
+//   512 tokens, 28672 -> 8192     624 / 322 / 269 / 236 / 324
+//  2048 tokens, 2560 -> 6912      256 / 162 / 118 / 106 / 85.6
+//   bfloat16 outputs
+//    64 tokens, 8192 -> 28672     106 / 58.6 / 58.0 / 69.5 / 78.0 / 109
+//   256 tokens, 2560 -> 6912     37.7 / 17.5 / 12.8 / 17.8 / 24.6 / 36.4
+//   512 tokens, 8192 -> 8192      198 / 74.5 / 53.8 / 42.7 / 61.4 / 81.5
+//  2048 tokens, 6912 -> 2560      345 / 97.9 / 73.7 / 70.9 / 53.6 / 88.5
+//  2048 tokens, 2560 -> 6912      245 / 132 / 89.5 / 75.3 / 55.7 / 46.9
+// The streaming kernel with 32 rows per block from 17 tokens on, where that leaves half the
+// CUs a block (32 tokens, 2560 -> 6912 9.9 -> 8.1, 8192 -> 28672 80.9 -> 72.9; 13 tokens, 6912
+// -> 2560 8.3 -> 11.7).
+inline F8Kernel f8_kernel(int64_t t, int64_t n, int64_t k, bool bf16, int cus) {
+  if (t <= 16) return kF8Few1;
+  const double blocks = (double)((k + 127) / 128), rows = (double)((t + 63) / 64) * (double)n * 1e-4;
+  F8Kernel best = t <= 32 && (n + 31) / 32 >= cus / 2 ? kF8Few2 : kF8Few1;
+  double least = t <= 32 ? 2.3 + 1.7 * rows + blocks * (0.14 + 0.22 * rows)
+                         : 2.8 + 3.6 * rows + blocks * (0.235 + 0.3 * rows);
+  struct Tile {
+    F8Kernel kernel;
+    int rows, tokens;
+    double block[2], round[2];                      // binary32, bfloat16 outputs
   };
-  const double cost[] = {(double)((t + 63) / 64) * (double)n * 7e-5 * (bf16 ? 1.3 : 1.0),
-                         rounds(128, 128) * (bf16 ? 0.85 : 1.2), rounds(256, 128) * (bf16 ? 1.2 : 1.95),
-                         rounds(256, 256) * 1.8};
-  const F8Kernel kernel[] = {few, kF8Split, kF8Wide, kF8Turns};
-  return kernel[std::min_element(cost, cost + (bf16 ? 4 : 3)) - cost];
+  static constexpr Tile kTiles[] = {
+      {kF8Small, 64, 64, {0.36, 0.29}, {4.2, 3.4}},    {kF8Tall, 128, 64, {0.59, 0.43}, {4.7, 3.5}},
+      {kF8Square, 128, 128, {0.96, 0.69}, {6.2, 3.9}}, {kF8Wide, 256, 128, {1.55, 0.98}, {10, 6.3}},
+      {kF8Turns, 256, 256, {0, 1.5}, {0, 8.7}}};
+  for (const Tile& c : kTiles) {
+    if (c.kernel == kF8Turns && !bf16) continue;
+    const int64_t tiles = ((n + c.rows - 1) / c.rows) * ((t + c.tokens - 1) / c.tokens);
+    const double time = (double)((tiles + cus - 1) / cus) * (blocks * c.block[bf16] + c.round[bf16]);
+    if (time < least) {
+      least = time;
+      best = c.kernel;
+    }
+  }
+  return best;
 }
 
 }  // namespace bl

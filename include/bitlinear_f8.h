@@ -63,7 +63,7 @@ bl_status bitlinear_unpack_weights_f8(const uint8_t* codes, const float* scales,
 /* y[t, n] = sum over blocks g of (x_scales[g, t] * w_scales[n / 128, g])
  *           * sum_{k in g} xq[t, k] * w[n, k].
  * BL_F32 outputs: products and sums in binary32.  BL_BF16 outputs of more than
- * 32 tokens may be formed by matrix instructions that cut each product of eight
+ * 16 tokens may be formed by matrix instructions that cut each product of eight
  * neighbouring k at 2^-13 of the largest of the eight, so within 7 * 2^-13 of the
  * sum of the products' magnitudes (4e-5 to 5e-5 of the result in the norm), before
  * they are rounded.  Sums go in an order that depends on the shape alone: the

@@ -19,38 +19,45 @@ def test_cases_reach_every_kernel(plan):
     seen = set()
     for t, n, k in SHAPES:
         for bf16 in (False, True):
-            kernel = plan(t, n, bf16, CUS)
+            kernel = plan(t, n, k, bf16, CUS)
             seen.add((kernel, bf16, k % 128 != 0))
             if kernel.startswith("few"):
                 seen.add((kernel, bf16, 1 if t <= 16 else 2 if t <= 32 else 4))
     for bf16 in (False, True):
-        for kernel in KERNELS[:5 if bf16 else 4]:
+        for kernel in KERNELS[:7 if bf16 else 6]:
             for tail in (False, True):
                 assert (kernel, bf16, tail) in seen, (kernel, bf16, tail)
-        for few in (("few1", 1), ("few1", 2), ("few1", 4), ("few2", 2), ("few2", 4)):
+        for few in (("few1", 1), ("few1", 2), ("few1", 4), ("few2", 2)):
             assert (few[0], bf16, few[1]) in seen, (few, bf16)
+
+
+KS = (16, 128, 2560, 28672, 131072)
 
 
 def test_binary32_outputs_never_take_the_e4m3_only_kernel(plan):
     for t in (1, 33, 64, 200, 1024, 4096, 1 << 24):
         for n in (1, 100, 2560, 28672, 128256, 1 << 26):
-            assert plan(t, n, False, CUS) != "turns"
+            for k in KS:
+                assert plan(t, n, k, False, CUS) != "turns"
 
 
 def test_few_tokens_stream(plan):
-    for t in range(1, 33):
+    for t in range(1, 17):
         for n in (1, 640, 128256, 1 << 26):
-            assert plan(t, n, True, CUS).startswith("few") and plan(t, n, False, CUS).startswith("few")
+            for k in KS:
+                assert plan(t, n, k, True, CUS) == plan(t, n, k, False, CUS) == "few1"
 
 
 @pytest.mark.parametrize("bf16", [False, True])
-@pytest.mark.parametrize("n", [1, 7, 16, 40, 130, 1000, 8192, 1 << 20, 1 << 26])
+@pytest.mark.parametrize("n", [1, 7, 16, 40, 130, 1000, 4097, 8192, 1 << 20, 1 << 26])
 def test_launches_fit(plan, n, bf16):
     """Fewer than 2^32 threads in any launch that T * N <= 2^36 allows."""
-    for t in (1, 16, 33, 64, 65, 1000, 1 << 14, 1 << 20, 1 << 24):
+    for t in (1, 16, 17, 32, 33, 64, 65, 1000, 1 << 14, 1 << 20, 1 << 24):
         if t * n > 1 << 36:
             continue
-        kernel = plan(t, n, bf16, CUS)
-        rows, tokens = {"few1": (16, 64), "few2": (32, 64), "split": (128, 128), "wide": (256, 128),
-                        "turns": (256, 256)}[kernel]
-        assert -(-n // rows) * -(-t // tokens) * 512 + 8 * 512 < 1 << 32, (kernel, t, n)
+        for k in KS:
+            kernel = plan(t, n, k, bf16, CUS)
+            rows, tokens, threads = {"few1": (16, 64, 512), "few2": (32, 64, 512), "small": (64, 64, 192),
+                                     "tall": (128, 64, 256), "square": (128, 128, 512),
+                                     "wide": (256, 128, 512), "turns": (256, 256, 512)}[kernel]
+            assert (-(-n // rows) * -(-t // tokens) + 8) * threads < 1 << 32, (kernel, t, n, k)
