@@ -18,7 +18,9 @@
 // Where both ends of the interval of +- 2^-44 (which covers the rounding of the
 // product with 1 / K and of the ends themselves) round to the same binary32,
 // that is ms; all steps from S to ms are monotonic.  Else, about one row in
-// 2^19, the row is summed again exactly, in buckets by exponent.
+// 2^19 (of short bfloat16 rows, whose sums have few bits, more: one in 1700 of 144), the
+// row is summed again exactly, in buckets by exponent (such a row of 144 5.9 us, any other
+// 3.9).
 //
 // Bound by memory (binary32 x, bfloat16 residual, int8 codes, 9 bytes an element:
 // 4096 x 2560 21.5 us, 4.4 TB/s; 1000 x 28672 56.8 us, 4.5; a large copy reaches 4.7), for
@@ -80,6 +82,7 @@ __global__ __launch_bounds__(1024) void k_add_subln(const Args a) {
   __shared__ double red_s[kMaxWaves];
   __shared__ int red_m[kMaxWaves], red_q[kMaxWaves];
   __shared__ unsigned long long hist[2][256];        // rare rows
+  __shared__ unsigned long long word[kLimbs];
   __shared__ uint32_t limb[kLimbs];
   __shared__ double exact;
   const int K = a.K, nvec = K >> 3;
@@ -197,6 +200,7 @@ __global__ __launch_bounds__(1024) void k_add_subln(const Args a) {
   float ms = (float)(mean * (1.0 - 0x1p-44));
   if (ms != (float)(mean * (1.0 + 0x1p-44))) {       // the same in every thread
     for (int j = tid; j < 512; j += nthr) (&hist[0][0])[j] = 0ull;
+    if (tid < kLimbs) word[tid] = 0ull;
     lds_sync();
     for (int v = tid; v < nvec; v += nthr) {
       float f[8];
@@ -215,11 +219,24 @@ __global__ __launch_bounds__(1024) void k_add_subln(const Args a) {
       }
     }
     lds_sync();
+    for (int j = tid; j < 512; j += nthr) {          // 32 bits at a time, carried afterwards
+      const int ex = j & 255;
+      const unsigned long long v = (&hist[0][0])[j];
+      if (!v || ex == 255) continue;                 // (not finite: no defined result)
+      const int at = 2 * ex + (j < 256 ? 22 : -2), l0 = at >> 5, o = at & 31;
+      const unsigned long long lo = v << o;
+      const uint32_t part[3] = {(uint32_t)lo, (uint32_t)(lo >> 32), o ? (uint32_t)(v >> (64 - o)) : 0u};
+#pragma unroll
+      for (int i = 0; i < 3; ++i)
+        if (part[i]) atomicAdd(&word[l0 + i], (unsigned long long)part[i]);
+    }
+    lds_sync();
     if (tid == 0) {
-      for (int i = 0; i < kLimbs; ++i) limb[i] = 0;
-      for (int ex = 1; ex < 255; ++ex) {
-        limbs_add(limb, hist[0][ex], 2 * ex + 22);
-        limbs_add(limb, hist[1][ex], 2 * ex - 2);
+      unsigned long long carry = 0;
+      for (int i = 0; i < kLimbs; ++i) {
+        carry += word[i];
+        limb[i] = (uint32_t)carry;
+        carry >>= 32;
       }
       exact = limbs_to_f64(limb, -298);
     }
