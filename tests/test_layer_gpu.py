@@ -107,7 +107,7 @@ def test_masks_and_ties(bl, t):
 def test_few_tokens_of_many_experts(bl, t, e, k):
     """Ties across a wave's 64 logits, experts that several tokens take at different
     ranks, tokens with fewer usable logits than k or none."""
-    layer = Layer(bl, e, 96, 272, 50)
+    layer = Layer(bl, e, 1040, 272, 50)
     x, logits = _tokens(t, 272, e)
     same = logits[:1].expand(t, e).contiguous()
     few = torch.full_like(logits, float("-inf"))
