@@ -151,9 +151,9 @@ __device__ __forceinline__ int expert_of_rank(const Keys& a, int E, int j, int w
 // expert have nothing to do while few tokens meet many experts; a block of a pair
 // first finds its expert, and ends if an earlier token takes the same one.
 // N rows of gate and up together; h by token * k + rank.
-// Bound by the start of its blocks and two loads one after the other (logits, then
-// weights: one token, 8 of 64 experts of 2560 -> 2 x 1024, 10.5 MB in 8.7 us), with
-// many experts by the stream of weights (16 tokens, 8 of 64, 75 MB in 18 us, 4.1 TB/s).
+// Bound by latency: the start of its blocks, the logits, then the tokens and the
+// weights (one token, 8 of 64 experts of 2560 -> 2 x 1024, 10.5 MB in 8.6 us; 16 tokens, 40 of
+// 64 taken, 53 MB in 18 us, where a third of the cycles issue vector instructions).
 template <int MODE, bool PAIRS, int U, int Q>
 __global__ __launch_bounds__(512) void k_layer_gate(const Router rt,
                                                     const uint32_t* __restrict__ packed,
@@ -313,9 +313,10 @@ __global__ __launch_bounds__(512) void k_layer_gate(const Router rt,
 // Down projections and the weighted sum (as k_experts_token): a block has one
 // token and 16 RT outputs, each of its k rows of h a team of `team` waves that
 // split K; the rows do not wait for the experts' numbers, the weights do.
-// (One token, 8 experts of 1024 -> 2560, 5.2 MB in 5.1 us: the latency of the number, the
-// weights and three barriers; 16 tokens 17 us, each expert's weights once per token
-// from the caches, 84 MB at 4.9 TB/s.)
+// (One token, 8 experts of 1024 -> 2560, 5.3 MB in 5.1 us: the latency of the number, the
+// weights and three barriers.  16 tokens 17 us: an expert's weights are read, from the
+// caches after the first time, and unpacked once per token, and each block quantises its
+// token's rows: vector instructions issue in over half of the cycles.)
 template <int RT, int U, int Q>
 __global__ __launch_bounds__(1024) void k_layer_down(const int32_t* __restrict__ ids,
                                                      const float* __restrict__ weights, int topk,

@@ -329,7 +329,9 @@ hipError_t launch(const Args& base, int64_t t, hipStream_t stream) {
   return e;
 }
 
-// e4m3 codes of tokens: 16 lanes per group of 128, one pass.
+// e4m3 codes of tokens: 16 lanes per group of 128, one pass.  Bound by memory (4096
+// tokens of 8192, bfloat16 22.3 us, 4.5 TB/s; binary32 31.3, 5.4), for few tokens by its
+// launch (13 of 6912 2.4 us).
 template <bool BF16>
 __global__ __launch_bounds__(256) void k_quant_f8(const void* __restrict__ x, int64_t T, int K,
                                                   int groups, int64_t units,
