@@ -79,34 +79,38 @@ __device__ __forceinline__ void store4(void* y, int64_t at, int n, int N, const 
 
 // ------------------------------------------------------------------ few tokens
 
-// Up to 16 TT tokens against 16 RT rows per block; the block's waves take the
-// blocks of K in turn and their sums meet in LDS, added in order of the waves.
-// Every load goes straight to registers, two blocks of K ahead of their use (four:
-// 128256 rows 82 us, two: 56).  Bound by the stream of weights (one token, 2560 ->
-// 128256: 328 MB in 55 us, 6.0 TB/s; a pure read stream reaches 6.2); with few rows by
-// latency (13 tokens, 6912 -> 2560: 17.7 MB in 8.3 us).
+// Up to 16 TT tokens against 16 RT rows per block or, not FULL, fewer, so that more CUs
+// have a block, which each take in some 24 GB/s (13 tokens, 6912 -> 2560, 12 rows 8.3 ->
+// 8.0 us; one token, 8192 -> 2000, 8 rows 7.4 -> 6.4, 8192 -> 128, 4 rows 7.0 -> 5.5).  The
+// block's waves take the blocks of K in turn and their sums meet in LDS, added in order
+// of the waves.  Every load goes straight to registers, two blocks of K ahead of its use
+// (four: 128256 rows 82 us, two: 56).  Bound by the stream of weights (one token, 2560 ->
+// 128256: 328 MB in 55 us, 6.0 TB/s; a pure read stream reaches 6.2), with few rows by what
+// a CU takes in and latency (13 tokens, 6912 -> 2560: 17.7 MB in 8.0 us).
 constexpr int kFewWaves = 8;
 constexpr int kFewAhead = 2;
 
-template <int TT, int RT, bool BF16>
+template <int TT, int RT, bool FULL, bool BF16>
 __global__ __launch_bounds__(64 * kFewWaves) void k_f8_few(const uint8_t* __restrict__ w,
                                                            const float* __restrict__ ws,
                                                            const uint8_t* __restrict__ xq,
                                                            const float* __restrict__ xs, int T,
-                                                           int N, int K, int t_tiles,
+                                                           int N, int K, int rows_, int t_tiles,
                                                            void* __restrict__ y) {
   constexpr int WV = kFewWaves, U = kFewAhead;
   __shared__ float red[WV][RT * TT][4][64];
   const int lane = threadIdx.x & 63, g = lane >> 4, r = lane & 15;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int kb_all = (K + kF8Block - 1) / kF8Block;
-  const int n0 = blockIdx.x / t_tiles * 16 * RT, t0 = blockIdx.x % t_tiles * 16 * TT;
-  const float* wsr = ws + (int64_t)(n0 / kF8Block) * kb_all;
+  const int rows = FULL ? 16 * RT : rows_;
+  const int n0 = blockIdx.x / t_tiles * rows, t0 = blockIdx.x % t_tiles * 16 * TT;
+  // one scale for the lane's outputs: four rows from a multiple of four on, or whole tiles
+  const float* wsr = ws + (int64_t)(min(n0 + (FULL ? 0 : 4 * g), N - 1) / kF8Block) * kb_all;
   const uint8_t* wrow[RT];
   const uint8_t* xrow[TT];
   int tok[TT];
 #pragma unroll
-  for (int i = 0; i < RT; ++i) wrow[i] = w + (int64_t)min(n0 + 16 * i + r, N - 1) * K;
+  for (int i = 0; i < RT; ++i) wrow[i] = w + (int64_t)min(n0 + min(16 * i + r, rows - 1), N - 1) * K;
 #pragma unroll
   for (int j = 0; j < TT; ++j) {
     tok[j] = min(t0 + 16 * j + r, T - 1);
@@ -203,7 +207,8 @@ __global__ __launch_bounds__(64 * kFewWaves) void k_f8_few(const uint8_t* __rest
 #pragma unroll
       for (int p = 1; p < WV; ++p) s[v] += red[p][q][v][lane];
     }
-    if (t < T) store4<BF16>(y, (int64_t)t * N, n0 + 16 * (q / TT) + 4 * g, N, s);
+    const int n = 16 * (q / TT) + 4 * g;
+    if (t < T && n < rows) store4<BF16>(y, (int64_t)t * N, n0 + n, N, s);
   }
 }
 
@@ -689,15 +694,18 @@ hipError_t forward(const uint8_t* w, const float* ws, const uint8_t* xq, const f
   switch (kernel) {
     case kF8Few1:
     case kF8Few2: {
-      const int rows = kernel == kF8Few1 ? 16 : 32;
+      const int rows = kernel == kF8Few2 ? 32 : f8_few_rows(n, device_cus());
       // fewer than 2^32 threads: many tokens come here with few rows only
       const int t_tiles = (int)((t + 63) / 64);
       const unsigned grid = (unsigned)((n + rows - 1) / rows * t_tiles);
-      auto* f = rows == 32 ? k_f8_few<2, 2, BF16>
-              : t <= 16    ? k_f8_few<1, 1, BF16>
-              : t <= 32    ? k_f8_few<2, 1, BF16>
-                           : k_f8_few<4, 1, BF16>;
-      f<<<grid, 64 * kFewWaves, 0, stream>>>(w, ws, xq, xs, (int)t, (int)n, (int)k, t_tiles, y);
+      auto few = [&](auto full) {
+        constexpr bool F = decltype(full)::value;
+        return t <= 16 ? k_f8_few<1, 1, F, BF16> : t <= 32 ? k_f8_few<2, 1, F, BF16> : k_f8_few<4, 1, F, BF16>;
+      };
+      auto* f = rows == 32 ? k_f8_few<2, 2, true, BF16>
+              : rows == 16 ? few(std::true_type{})
+                           : few(std::false_type{});
+      f<<<grid, 64 * kFewWaves, 0, stream>>>(w, ws, xq, xs, (int)t, (int)n, (int)k, rows, t_tiles, y);
       return hipGetLastError();
     }
     case kF8Turns:

@@ -7,7 +7,7 @@
 namespace bl {
 
 enum F8Kernel {
-  kF8Few1,     // k_f8_few, 16 rows per block
+  kF8Few1,     // k_f8_few, up to 16 rows per block
   kF8Few2,     // k_f8_few, 32 rows per block (17 to 32 tokens)
   kF8Small,    // k_f8_tile, 64 x 64, three groups of waves that share K
   kF8Tall,     // k_f8_tile, 128 x 64, two groups
@@ -64,6 +64,13 @@ inline F8Kernel f8_kernel(int64_t t, int64_t n, int64_t k, bool bf16, int cus) {
     }
   }
   return best;
+}
+
+// Rows per block of kF8Few1, a multiple of four: as few as make no more blocks than CUs.
+inline int f8_few_rows(int64_t n, int cus) {
+  for (int rows = 4; rows < 16; rows += 4)
+    if ((n + rows - 1) / rows <= cus) return rows;
+  return 16;
 }
 
 }  // namespace bl

@@ -9,26 +9,39 @@ CUS = 256
 
 
 @pytest.fixture(scope="module")
-def plan(tmp_path_factory):
+def both(tmp_path_factory):
     return compiled(str(tmp_path_factory.mktemp("f8_plan")))
 
 
-def test_cases_reach_every_kernel(plan):
+@pytest.fixture(scope="module")
+def plan(both):
+    return both[0]
+
+
+def test_cases_reach_every_kernel(both):
     """Both output types, whole and partial last blocks of K; of the streaming
-    kernel every number of token tiles."""
+    kernel every number of token tiles and of rows per block."""
+    plan, rows = both
     seen = set()
     for t, n, k in SHAPES:
         for bf16 in (False, True):
             kernel = plan(t, n, k, bf16, CUS)
             seen.add((kernel, bf16, k % 128 != 0))
             if kernel.startswith("few"):
-                seen.add((kernel, bf16, 1 if t <= 16 else 2 if t <= 32 else 4))
+                tiles = 1 if t <= 16 else 2 if t <= 32 else 4
+                seen.add((kernel, bf16, tiles))
+                if kernel == "few1":
+                    seen.add((bf16, tiles, rows(n, CUS)))
     for bf16 in (False, True):
         for kernel in KERNELS[:7 if bf16 else 6]:
             for tail in (False, True):
                 assert (kernel, bf16, tail) in seen, (kernel, bf16, tail)
         for few in (("few1", 1), ("few1", 2), ("few1", 4), ("few2", 2)):
             assert (few[0], bf16, few[1]) in seen, (few, bf16)
+        for tiles in (1, 2, 4):
+            # (bfloat16 outputs of more than 32 tokens take tiles from about 2000 rows on)
+            for per in (4, 8) if bf16 and tiles == 4 else (4, 8, 12, 16):
+                assert (bf16, tiles, per) in seen, (bf16, tiles, per)
 
 
 KS = (16, 128, 2560, 28672, 131072)
@@ -61,3 +74,12 @@ def test_launches_fit(plan, n, bf16):
                                      "tall": (128, 64, 256), "square": (128, 128, 512),
                                      "wide": (256, 128, 512), "turns": (256, 256, 512)}[kernel]
             assert (-(-n // rows) * -(-t // tokens) + 8) * threads < 1 << 32, (kernel, t, n, k)
+
+
+def test_rows_per_block(both):
+    """Multiples of four, no more blocks than CUs below 16 rows."""
+    for cus in (1, 64, 256):
+        for n in (1, 4, 1024, 1025, 2048, 2049, 4095, 4096, 1 << 26):
+            rows = both[1](n, cus)
+            assert rows in (4, 8, 12, 16) and (rows == 16 or -(-n // rows) <= cus)
+            assert rows == 4 or -(-n // (rows - 4)) > cus
