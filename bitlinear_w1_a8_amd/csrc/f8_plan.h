@@ -66,10 +66,11 @@ inline F8Kernel f8_kernel(int64_t t, int64_t n, int64_t k, bool bf16, int cus) {
   return best;
 }
 
-// Rows per block of kF8Few1, a multiple of four: as few as make no more blocks than CUs.
-inline int f8_few_rows(int64_t n, int cus) {
+// Rows per block of kF8Few1, a multiple of four: as few as make no more blocks than CUs
+// (which also keeps a launch of many tokens below 2^32 threads).
+inline int f8_few_rows(int64_t t, int64_t n, int cus) {
   for (int rows = 4; rows < 16; rows += 4)
-    if ((n + rows - 1) / rows <= cus) return rows;
+    if ((n + rows - 1) / rows * ((t + 63) / 64) <= cus) return rows;
   return 16;
 }
 

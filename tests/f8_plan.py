@@ -11,14 +11,14 @@ SOURCE = """
 extern "C" int plan(int64_t t, int64_t n, int64_t k, int bf16, int cus) {
   return bl::f8_kernel(t, n, k, bf16, cus);
 }
-extern "C" int rows(int64_t n, int cus) { return bl::f8_few_rows(n, cus); }
+extern "C" int rows(int64_t t, int64_t n, int cus) { return bl::f8_few_rows(t, n, cus); }
 """
 
 KERNELS = ("few1", "few2", "small", "tall", "square", "wide", "turns")
 
 
 def compiled(folder):
-    """f8_kernel(T, N, K, bfloat16 outputs, CUs) -> its name, and f8_few_rows(N, CUs), from a
+    """f8_kernel(T, N, K, bfloat16 outputs, CUs) -> its name, and f8_few_rows(T, N, CUs), from a
     library built in `folder`."""
     src, lib = os.path.join(folder, "plan.cpp"), os.path.join(folder, "plan.so")
     with open(src, "w") as f:
@@ -26,6 +26,6 @@ def compiled(folder):
     subprocess.run(["g++", "-std=c++17", "-O1", "-shared", "-fPIC", "-I", build.CSRC, src, "-o", lib], check=True)
     built = ctypes.CDLL(lib)
     fn, rows = built.plan, built.rows
-    rows.argtypes = [ctypes.c_int64, ctypes.c_int]
+    rows.argtypes = [ctypes.c_int64, ctypes.c_int64, ctypes.c_int]
     fn.argtypes = [ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, ctypes.c_int, ctypes.c_int]
     return lambda t, n, k, bf16, cus: KERNELS[fn(t, n, k, int(bf16), cus)], rows

@@ -31,7 +31,7 @@ def test_cases_reach_every_kernel(both):
                 tiles = 1 if t <= 16 else 2 if t <= 32 else 4
                 seen.add((kernel, bf16, tiles))
                 if kernel == "few1":
-                    seen.add((bf16, tiles, rows(n, CUS)))
+                    seen.add((bf16, tiles, rows(t, n, CUS)))
     for bf16 in (False, True):
         for kernel in KERNELS[:7 if bf16 else 6]:
             for tail in (False, True):
@@ -63,14 +63,15 @@ def test_few_tokens_stream(plan):
 
 @pytest.mark.parametrize("bf16", [False, True])
 @pytest.mark.parametrize("n", [1, 7, 16, 40, 130, 1000, 4097, 8192, 1 << 20, 1 << 26])
-def test_launches_fit(plan, n, bf16):
+def test_launches_fit(both, n, bf16):
     """Fewer than 2^32 threads in any launch that T * N <= 2^36 allows."""
+    plan, few_rows = both
     for t in (1, 16, 17, 32, 33, 64, 65, 1000, 1 << 14, 1 << 20, 1 << 24):
         if t * n > 1 << 36:
             continue
         for k in KS:
             kernel = plan(t, n, k, bf16, CUS)
-            rows, tokens, threads = {"few1": (16, 64, 512), "few2": (32, 64, 512), "small": (64, 64, 192),
+            rows, tokens, threads = {"few1": (few_rows(t, n, CUS), 64, 512), "few2": (32, 64, 512), "small": (64, 64, 192),
                                      "tall": (128, 64, 256), "square": (128, 128, 512),
                                      "wide": (256, 128, 512), "turns": (256, 256, 512)}[kernel]
             assert (-(-n // rows) * -(-t // tokens) + 8) * threads < 1 << 32, (kernel, t, n, k)
@@ -80,6 +81,7 @@ def test_rows_per_block(both):
     """Multiples of four, no more blocks than CUs below 16 rows."""
     for cus in (1, 64, 256):
         for n in (1, 4, 1024, 1025, 2048, 2049, 4095, 4096, 1 << 26):
-            rows = both[1](n, cus)
-            assert rows in (4, 8, 12, 16) and (rows == 16 or -(-n // rows) <= cus)
-            assert rows == 4 or -(-n // (rows - 4)) > cus
+            for t in (1, 64, 65, 1000, 1 << 24):
+                lots, rows = -(-t // 64), both[1](t, n, cus)
+                assert rows in (4, 8, 12, 16) and (rows == 16 or -(-n // rows) * lots <= cus)
+                assert rows == 4 or -(-n // (rows - 4)) * lots > cus
