@@ -58,7 +58,8 @@ bl_status check_product(const char* fn, const uint8_t* w, const float* w_scales,
                         int y_dtype) {
   if (!w || !w_scales || !xq || !x_scales || !y)
     return fail(BL_ERR_NULL, "%s: NULL pointer argument", fn);
-  if (bl_status rc = check_dtype(fn, "y_dtype", y_dtype)) return rc;
+  if (y_dtype != (BL_BF16 | BL_CUT_SUMS))
+    if (bl_status rc = check_dtype(fn, "y_dtype", y_dtype)) return rc;
   if (bl_status rc = check_matrix(fn, n, k)) return rc;
   if (t < 1 || t > kMaxT || t > kMaxTN / n)
     return fail(BL_ERR_SHAPE, "%s: T=%lld out of range", fn, (long long)t);
@@ -130,7 +131,7 @@ bl_status bitlinear_forward_f8(const uint8_t* w, const float* w_scales, const ui
                                int y_dtype, void* stream) {
   const char* fn = "bitlinear_forward_f8";
   if (bl_status rc = check_product(fn, w, w_scales, xq, x_scales, T, N, K, y, y_dtype)) return rc;
-  return launched(fn, bl::launch_forward_f8(w, w_scales, xq, x_scales, T, N, K, y, y_dtype == BL_BF16,
+  return launched(fn, bl::launch_forward_f8(w, w_scales, xq, x_scales, T, N, K, y, y_dtype,
                                             static_cast<hipStream_t>(stream)));
 }
 
@@ -145,7 +146,7 @@ bl_status bitlinear_linear_f8(const void* x, int x_dtype, const uint8_t* w, cons
   const hipStream_t s = static_cast<hipStream_t>(stream);
   hipError_t e = bl::launch_quant_f8(x, x_dtype == BL_BF16, T, K, xq, x_scales, s);
   if (e == hipSuccess)
-    e = bl::launch_forward_f8(w, w_scales, xq, x_scales, T, N, K, y, y_dtype == BL_BF16, s);
+    e = bl::launch_forward_f8(w, w_scales, xq, x_scales, T, N, K, y, y_dtype, s);
   return launched(fn, e);
 }
 

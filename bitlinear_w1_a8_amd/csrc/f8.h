@@ -37,8 +37,8 @@ hipError_t launch_pack_f8(const float* w, int64_t n, int64_t k, uint8_t* codes, 
 hipError_t launch_unpack_f8(const uint8_t* codes, const float* scales, int64_t n, int64_t k,
                             float* w, hipStream_t stream);
 hipError_t launch_forward_f8(const uint8_t* w, const float* ws, const uint8_t* xq, const float* xs,
-                             int64_t t, int64_t n, int64_t k, void* y, int bf16,
-                             hipStream_t stream);
+                             int64_t t, int64_t n, int64_t k, void* y, int y_dtype,
+                             hipStream_t stream);   // y_dtype with or without BL_CUT_SUMS
 
 // ---------------------------------------------------------------- device helpers
 

@@ -8,13 +8,13 @@
 //
 // Two kinds of matrix instruction.  The e4m3 ones (v_mfma_f32_32x32x64_f8f6f4, 2048
 // multiply-adds per cycle and SIMD counted as flops) add the products of eight
-// neighbouring k with what lies 2^14 and more below the largest of the eight cut
-// off, measured on 16x16x128, 16x16x32, 32x32x64 and 32x32x16 alike: a sum is off by up
-// to 7 * 2^-13 of its magnitudes' sum (seen: 2^-12.7; 4e-5 to 5e-5 in the norm), more
-// than a binary32 result may be and a fortieth of what its rounding to bfloat16
-// costs.  The f16 ones at half the rate hold every e4m3 exactly and add in binary32
-// (8e-8 in the norm).  So binary32 outputs, and batches that the stream of
-// weights bounds, take the f16 ones; bfloat16 outputs of many tokens the e4m3 ones.
+// neighbouring k (8 i .. 8 i + 7) with all bits below 2^-13 of the largest one's power of
+// two (its factors' exponents added) cut off, towards zero; measured on 16x16x128,
+// 16x16x32, 32x32x64 and 32x32x16 alike.  Each of the other seven loses less than 2^-13 of
+// the largest, so a sum is off by up to 7 * 2^-13 of its magnitudes' sum (seen: 2^-12.7; 4e-5
+// to 5e-5 in the norm), which is more than sums in binary32 may be.  The f16 ones at half the
+// rate hold every e4m3 exactly and add in binary32 (8e-8 in the norm).  So products take
+// the f16 ones, and the e4m3 ones only where the caller has asked for cut sums.
 #include <algorithm>
 #include <type_traits>
 
@@ -325,7 +325,7 @@ using S2 = std::integral_constant<int, 2>;
 // (6912 -> 2560, 256 tokens, binary32 outputs: 64 x 64 in two groups with three buffers 27.1 us,
 // in four with two 24.6, in three with three 22.4; 128 x 64 in two with three 32.7; 128 x 128 in
 // two with two 50.)
-// NATIVE: e4m3 instructions; else each wave widens its operands to f16.
+// NATIVE: e4m3 instructions (cut sums); else each wave widens its operands to f16.
 template <bool BF16, bool NATIVE, bool TAIL, int WR, int WT, int GROUPS, int STAGES>
 __global__ __launch_bounds__(64 * WR * WT * GROUPS) void k_f8_tile(
     const uint8_t* __restrict__ w, const float* __restrict__ ws, const uint8_t* __restrict__ xq,
@@ -487,7 +487,7 @@ __global__ __launch_bounds__(64 * WR * WT * GROUPS) void k_f8_tile(
       store_tile<BF16>(acc[i][j], y, t0 + wt + 32 * j + c, n0 + wr + 32 * i, h, T, N);
 }
 
-// 256 x 256 tiles with the e4m3 instructions: 2 x 4 waves of 128 x 64 in two groups of
+// 256 x 256 tiles with the e4m3 instructions (cut sums, bfloat16 outputs): 2 x 4 waves of 128 x 64 in two groups of
 // four, one wave of each on a SIMD, in turn.  While one group runs its matrix
 // instructions (phase M) the other scales its last sums, reads its next operands from
 // LDS and sends for the next block of K (phase L); a barrier ends each phase.  A wave
@@ -679,18 +679,18 @@ hipError_t launch_tiles(F whole, F tail, int threads, const uint8_t* w, const fl
   return hipGetLastError();
 }
 
-template <bool BF16, int WR, int WT, int GROUPS, int STAGES>
+template <bool BF16, bool CUT, int WR, int WT, int GROUPS, int STAGES>
 hipError_t launch_tile(const uint8_t* w, const float* ws, const uint8_t* xq, const float* xs, int64_t t,
                        int64_t n, int64_t k, void* y, hipStream_t stream) {
-  return launch_tiles<64 * WR, 64 * WT>(k_f8_tile<BF16, BF16, false, WR, WT, GROUPS, STAGES>,
-                                        k_f8_tile<BF16, BF16, true, WR, WT, GROUPS, STAGES>,
+  return launch_tiles<64 * WR, 64 * WT>(k_f8_tile<BF16, CUT, false, WR, WT, GROUPS, STAGES>,
+                                        k_f8_tile<BF16, CUT, true, WR, WT, GROUPS, STAGES>,
                                         64 * WR * WT * GROUPS, w, ws, xq, xs, t, n, k, y, stream);
 }
 
-template <bool BF16>
+template <bool BF16, bool CUT>
 hipError_t forward(const uint8_t* w, const float* ws, const uint8_t* xq, const float* xs, int64_t t,
                    int64_t n, int64_t k, void* y, hipStream_t stream) {
-  const F8Kernel kernel = f8_kernel(t, n, k, BF16, device_cus());
+  const F8Kernel kernel = f8_kernel(t, n, k, CUT, device_cus());
   switch (kernel) {
     case kF8Few1:
     case kF8Few2: {
@@ -710,20 +710,21 @@ hipError_t forward(const uint8_t* w, const float* ws, const uint8_t* xq, const f
     }
     case kF8Turns:
       return launch_tiles<256, 256>(k_f8_turns<false>, k_f8_turns<true>, 512, w, ws, xq, xs, t, n, k, y, stream);
-    case kF8Wide: return launch_tile<BF16, 4, 2, 1, 3>(w, ws, xq, xs, t, n, k, y, stream);
-    case kF8Square: return launch_tile<BF16, 2, 2, 2, 2>(w, ws, xq, xs, t, n, k, y, stream);
-    case kF8Tall: return launch_tile<BF16, 2, 1, 2, 3>(w, ws, xq, xs, t, n, k, y, stream);
-    default: return launch_tile<BF16, 1, 1, 3, 3>(w, ws, xq, xs, t, n, k, y, stream);
+    case kF8Wide: return launch_tile<BF16, CUT, 4, 2, 1, 3>(w, ws, xq, xs, t, n, k, y, stream);
+    case kF8Square: return launch_tile<BF16, CUT, 2, 2, 2, 2>(w, ws, xq, xs, t, n, k, y, stream);
+    case kF8Tall: return launch_tile<BF16, CUT, 2, 1, 2, 3>(w, ws, xq, xs, t, n, k, y, stream);
+    default: return launch_tile<BF16, CUT, 1, 1, 3, 3>(w, ws, xq, xs, t, n, k, y, stream);
   }
 }
 
 }  // namespace
 
 hipError_t launch_forward_f8(const uint8_t* w, const float* ws, const uint8_t* xq, const float* xs,
-                             int64_t t, int64_t n, int64_t k, void* y, int bf16,
+                             int64_t t, int64_t n, int64_t k, void* y, int y_dtype,
                              hipStream_t stream) {
-  return bf16 ? forward<true>(w, ws, xq, xs, t, n, k, y, stream)
-              : forward<false>(w, ws, xq, xs, t, n, k, y, stream);
+  return y_dtype == BL_F32    ? forward<false, false>(w, ws, xq, xs, t, n, k, y, stream)
+         : y_dtype == BL_BF16 ? forward<true, false>(w, ws, xq, xs, t, n, k, y, stream)
+                              : forward<true, true>(w, ws, xq, xs, t, n, k, y, stream);
 }
 
 hipError_t launch_pack_f8(const float* w, int64_t n, int64_t k, uint8_t* codes, float* scales,

@@ -19,6 +19,8 @@ SIGNATURES = {
                                      _c_vp, _c_int, _c_vp]),
 }
 
+#: what a product's sums keep: binary32, or (bfloat16 outputs) what e4m3 matrix instructions keep
+SUMS = {"full": 0, "cut": 0x100}             # BL_CUT_SUMS
 _DTYPES = {torch.float32: BL_F32, torch.bfloat16: BL_BF16}
 _F8 = torch.float8_e4m3fn
 
@@ -89,16 +91,23 @@ def unpack_weights_f8(w, w_scales):
     return out
 
 
-def _out(dev, out, shape, dtype, on):
+def _out(dev, out, shape, dtype, on, sums):
+    """The outputs' tensor, and the C ABI's y_dtype."""
+    if out is not None:
+        device_of(out, "out")
+        dtype = out.dtype
+    kind = _DTYPES.get(dtype)
+    if kind is None:
+        raise TypeError(f"{'dtype' if out is None else 'out'} must be float32 or bfloat16, got {dtype}")
+    if sums not in SUMS:
+        raise ValueError(f"sums must be one of {sorted(SUMS)}, got {sums!r}")
+    if sums == "cut" and kind != BL_BF16:
+        raise ValueError("cut sums are for bfloat16 outputs")
     if out is None:
-        if dtype not in _DTYPES:
-            raise TypeError(f"dtype must be float32 or bfloat16, got {dtype}")
-        return torch.empty(shape, dtype=dtype, device=on)
-    device_of(out, "out")
-    if out.dtype not in _DTYPES:
-        raise TypeError(f"out must be float32 or bfloat16, got {out.dtype}")
-    need(dev, out, "out", out.dtype, shape)
-    return out
+        out = torch.empty(shape, dtype=dtype, device=on)
+    else:
+        need(dev, out, "out", dtype, shape)
+    return out, kind | SUMS[sums]
 
 
 def _rows(w, k):
@@ -109,10 +118,12 @@ def _rows(w, k):
     return w.shape[0]
 
 
-def forward_f8(w, w_scales, xq, x_scales, dtype=torch.float32, out=None):
+def forward_f8(w, w_scales, xq, x_scales, dtype=torch.float32, out=None, sums="full"):
     """y [T, N] of ``dtype`` (float32 or bfloat16; ``out`` brings its own) =
     tokens (xq float8_e4m3fn [T, K], x_scales float32 [ceil(K / 128), T], from
-    quant_act_f8 or add_subln_quant_act_f8) times a matrix of pack_weights_f8."""
+    quant_act_f8 or add_subln_quant_act_f8) times a matrix of pack_weights_f8,
+    summed in binary32.  ``sums="cut"`` allows bfloat16 outputs to be formed
+    faster from sums that lose up to 7 * 2^-13 of their products' magnitudes."""
     lib = _load()
     dev = device_of(xq, "xq")
     if xq.dim() != 2:
@@ -123,13 +134,13 @@ def forward_f8(w, w_scales, xq, x_scales, dtype=torch.float32, out=None):
     need(dev, w, "w", _F8, (n, k))
     need(dev, w_scales, "w_scales", torch.float32, (_blocks(n), _blocks(k)))
     need(dev, x_scales, "x_scales", torch.float32, (_blocks(k), t))
-    out = _out(dev, out, (t, n), dtype, xq.device)
+    out, kind = _out(dev, out, (t, n), dtype, xq.device, sums)
     call(dev, lib.bitlinear_forward_f8, w.data_ptr(), w_scales.data_ptr(), xq.data_ptr(),
-         x_scales.data_ptr(), t, n, k, out.data_ptr(), _DTYPES[out.dtype])
+         x_scales.data_ptr(), t, n, k, out.data_ptr(), kind)
     return out
 
 
-def linear_f8(x, w, w_scales, dtype=torch.float32, out=None):
+def linear_f8(x, w, w_scales, dtype=torch.float32, out=None, sums="full"):
     """quant_act_f8 of x [T, K] (float32 or bfloat16), then forward_f8: y [T, N]."""
     lib = _load()
     dev = device_of(x, "x")
@@ -144,10 +155,10 @@ def linear_f8(x, w, w_scales, dtype=torch.float32, out=None):
     need(dev, w, "w", _F8, (n, k))
     need(dev, w_scales, "w_scales", torch.float32, (_blocks(n), blocks))
     on = x.device
-    out = _out(dev, out, (t, n), dtype, on)
+    out, kind = _out(dev, out, (t, n), dtype, on, sums)
     codes = (t * k + 255) & ~255                # the codes, then their scales, in one piece
     scratch = torch.empty(codes + 4 * blocks * t, dtype=torch.uint8, device=on)
     at = scratch.data_ptr()
     call(dev, lib.bitlinear_linear_f8, x.data_ptr(), dt, w.data_ptr(), w_scales.data_ptr(), t, n, k, at,
-         at + codes, out.data_ptr(), _DTYPES[out.dtype])
+         at + codes, out.data_ptr(), kind)
     return out

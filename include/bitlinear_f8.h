@@ -62,19 +62,25 @@ bl_status bitlinear_unpack_weights_f8(const uint8_t* codes, const float* scales,
 
 /* y[t, n] = sum over blocks g of (x_scales[g, t] * w_scales[n / 128, g])
  *           * sum_{k in g} xq[t, k] * w[n, k].
- * BL_F32 outputs: products and sums in binary32.  BL_BF16 outputs of more than
- * 16 tokens may be formed by matrix instructions that cut each product of eight
- * neighbouring k at 2^-13 of the largest of the eight, so within 7 * 2^-13 of the
- * sum of the products' magnitudes (4e-5 to 5e-5 of the result in the norm), before
- * they are rounded.  Sums go in an order that depends on the shape alone: the
- * same inputs give the same bits on every call.
+ * Products and sums in binary32, for either type of output and any number of
+ * tokens.  Sums go in an order that depends on the shape alone: the same inputs
+ * give the same bits on every call.
+ *
+ * With BL_CUT_SUMS (BL_BF16 | BL_CUT_SUMS as y_dtype) the caller allows matrix
+ * instructions of twice the rate that keep fewer bits: of eight products of
+ * neighbouring k (8 i .. 8 i + 7) all bits below 2^-13 of the largest one's power of
+ * two are cut off, so a sum is within 7 * 2^-13 of its products' magnitudes (4e-5
+ * to 5e-5 of the result in the norm, for activations without outlying features)
+ * before it is rounded to bfloat16.  Few tokens may be summed in binary32 all the same.
  *
  *   w, w_scales   as bitlinear_pack_weights_f8 writes them.
  *   xq, x_scales  as bitlinear_quant_act_f8 writes them; both code arrays 16-byte aligned.
  *   T, N, K  1 <= T <= 2^24, T * N <= 2^36, N and K as bitlinear_pack_weights_f8.
- *   y_dtype  BL_F32, or BL_BF16 (the binary32 result rounded to nearest even).
+ *   y_dtype  BL_F32, or BL_BF16 (the binary32 result rounded to nearest even), the latter
+ *            with or without BL_CUT_SUMS.
  *   y        [T, N] output, aligned to its element.
  * Errors: BL_ERR_NULL, BL_ERR_SHAPE, BL_ERR_ALIGN, BL_ERR_DTYPE, BL_ERR_HIP. */
+#define BL_CUT_SUMS 0x100
 bl_status bitlinear_forward_f8(const uint8_t* w, const float* w_scales, const uint8_t* xq,
                                const float* x_scales, int64_t T, int64_t N, int64_t K, void* y,
                                int y_dtype, void* stream);
