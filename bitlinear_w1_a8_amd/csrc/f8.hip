@@ -695,7 +695,6 @@ hipError_t forward(const uint8_t* w, const float* ws, const uint8_t* xq, const f
     case kF8Few1:
     case kF8Few2: {
       const int rows = kernel == kF8Few2 ? 32 : f8_few_rows(t, n, device_cus());
-      // fewer than 2^32 threads: many tokens come here with few rows only
       const int t_tiles = (int)((t + 63) / 64);
       const unsigned grid = (unsigned)((n + rows - 1) / rows * t_tiles);
       auto few = [&](auto full) {

@@ -19,7 +19,8 @@ enum F8Kernel {
 // Up to 16 tokens the streaming kernel, beyond them the least of these estimates, in
 // microseconds.  A kernel of tiles takes rounds of one tile per CU, each of them a
 // time per block of 128 k and one for its start and end; the streaming kernel grows
-// with rows and lots of 64 tokens.  Fitted to graph replays of every kernel at 138
+// with rows and lots of 64 tokens per CU, and a launch of it has fewer than 2^32 threads
+// (tiles always have, as T * N <= 2^36).  Fitted to graph replays of every kernel at 138
 // sizes (8 to 2048 tokens) with weights from memory; what the rule takes was 0.8%
 // behind the fastest on average, 15% at most.  Some of them, streaming / 64 x 64 / 128 x
 // 64 / 128 x 128 / 256 x 128 / 256 x 256:
@@ -41,10 +42,13 @@ enum F8Kernel {
 // -> 2560 8.3 -> 11.7).
 inline F8Kernel f8_kernel(int64_t t, int64_t n, int64_t k, bool cut, int cus) {
   if (t <= 16) return kF8Few1;
-  const double blocks = (double)((k + 127) / 128), rows = (double)((t + 63) / 64) * (double)n * 1e-4;
+  const int64_t lots = (t + 63) / 64;
+  const double blocks = (double)((k + 127) / 128);
+  const double rows = (double)lots * (double)n * 1e-4 * (256.0 / cus);   // (fitted on 256 CUs)
   F8Kernel best = t <= 32 && (n + 31) / 32 >= cus / 2 ? kF8Few2 : kF8Few1;
   double least = t <= 32 ? 2.3 + 1.7 * rows + blocks * (0.14 + 0.22 * rows)
                          : 2.8 + 3.6 * rows + blocks * (0.235 + 0.3 * rows);
+  if ((n + 15) / 16 * lots >= int64_t(1) << 23) least = 1e300;           // of 512 threads each
   struct Tile {
     F8Kernel kernel;
     int rows, tokens;
@@ -66,8 +70,7 @@ inline F8Kernel f8_kernel(int64_t t, int64_t n, int64_t k, bool cut, int cus) {
   return best;
 }
 
-// Rows per block of kF8Few1, a multiple of four: as few as make no more blocks than CUs
-// (which also keeps a launch of many tokens below 2^32 threads).
+// Rows per block of kF8Few1, a multiple of four: as few as make no more blocks than CUs.
 inline int f8_few_rows(int64_t t, int64_t n, int cus) {
   for (int rows = 4; rows < 16; rows += 4)
     if ((n + rows - 1) / rows * ((t + 63) / 64) <= cus) return rows;
