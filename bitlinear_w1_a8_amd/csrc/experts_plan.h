@@ -29,4 +29,8 @@ inline int few_depth(int64_t k) {
   return (int)std::min<int64_t>((chunks + 1) / 2 * 2, 10);
 }
 
+// LDS row stride of int8 activations: whole chunks of 256 k, zero past K, and
+// 16 bytes that spread the rows of one operand read over the banks.
+constexpr int few_stride(int k) { return ((k + 255) & ~255) + 16; }
+
 }  // namespace bl

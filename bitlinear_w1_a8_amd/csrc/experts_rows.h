@@ -62,10 +62,6 @@ __device__ __forceinline__ v4i operand(uint32_t w) {
   return v4i{(int)codes_of(w, 0), (int)codes_of(w, 1), (int)codes_of(w, 2), (int)codes_of(w, 3)};
 }
 
-// LDS row stride of int8 activations: whole chunks of 256 k, zero past K, and
-// 16 bytes that spread the rows of one operand read over the banks.
-__host__ __device__ constexpr int few_stride(int k) { return ((k + 255) & ~255) + 16; }
-
 // 16 weight rows (lane (qg, r) takes 64 k, 16 bytes, of row r per chunk) against
 // up to 16 int8 rows in LDS over all of K; w holds the row's first U chunks and
 // is filled again as it empties.  x: the lane's row, at 64 qg.

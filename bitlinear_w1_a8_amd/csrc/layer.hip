@@ -14,16 +14,11 @@
 #include <type_traits>
 
 #include "experts_rows.h"
+#include "layer_plan.h"
 #include "route_keys.h"
 
 namespace bl {
 namespace {
-
-constexpr int kTokens = 16;        // most tokens of the two launches: the columns of an MFMA
-constexpr int kRawTokens = 6;      // most whose step A1 every block repeats
-constexpr int kPairTokens = 4;     // most whose blocks belong to (token, rank) pairs
-constexpr int kTopK = 16;          // most experts per token: one DPP row
-constexpr int kLayerExperts = 256; // most experts: 16 logits per lane of a row
 
 struct Router {
   const void* logits;
@@ -163,7 +158,7 @@ __global__ __launch_bounds__(512) void k_layer_gate(const Router rt,
                                                     const float* __restrict__ absmax, int N, int K,
                                                     uint16_t* __restrict__ h) {
   extern __shared__ __align__(16) unsigned char xs[];   // [T][few_stride(K)], then raw [T][K]
-  __shared__ int rank[kTokens], qsum[kTokens], amax[kTokens];
+  __shared__ int rank[kLayerTokens], qsum[kLayerTokens], amax[kLayerTokens];
   if (blockIdx.y == 0) {
     if (blockIdx.x == 0) choose_rows(rt);
     return;
@@ -173,7 +168,7 @@ __global__ __launch_bounds__(512) void k_layer_gate(const Router rt,
   const int qg = lane >> 4, r = lane & 15;
 
   // ranks of the block's expert: -1 where a token does not take it
-  if (tid < kTokens) {
+  if (tid < kLayerTokens) {
     rank[tid] = -1;
     qsum[tid] = amax[tid] = 0;
   }
@@ -326,8 +321,8 @@ __global__ __launch_bounds__(1024) void k_layer_down(const int32_t* __restrict__
                                                      const uint16_t* __restrict__ h, int N, int K,
                                                      float* __restrict__ y) {
   extern __shared__ __align__(16) unsigned char xs[];   // [topk][few_stride(K)]
-  __shared__ int amax[kTopK], tile[kTopK][16 * RT];
-  __shared__ float scale[kTopK], share[kTopK];
+  __shared__ int amax[kLayerTopK], tile[kLayerTopK][16 * RT];
+  __shared__ float scale[kLayerTopK], share[kLayerTopK];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int qg = lane >> 4, r = lane & 15;
@@ -335,8 +330,8 @@ __global__ __launch_bounds__(1024) void k_layer_down(const int32_t* __restrict__
   const int j = wave / team, part = wave - j * team;
   const int K16 = K >> 4, nchunks = (K + 255) >> 8, stride = few_stride(K);
   const int per = (nchunks + team - 1) / team, c0 = part * per, c1 = min(c0 + per, nchunks);
-  for (int i = tid; i < kTopK * 16 * RT; i += blockDim.x) (&tile[0][0])[i] = 0;
-  if (tid < kTopK) amax[tid] = 0;
+  for (int i = tid; i < kLayerTopK * 16 * RT; i += blockDim.x) (&tile[0][0])[i] = 0;
+  if (tid < kLayerTopK) amax[tid] = 0;
 
   const int pair = t * topk + j;
   const void* xrow = h + (int64_t)pair * K;
@@ -473,26 +468,19 @@ struct Layout {
   }
 };
 
-size_t rows_lds(int64_t k, int64_t rows, int mode) {
-  return (size_t)rows * (few_stride((int)k) + (mode == kInt8 ? 0 : mode == kBf16 ? 2 * k : 4 * k));
-}
-
 template <int MODE, bool PAIRS>
-hipError_t launch_gate(const LayerCall& c, const Router& rt, const void* x, const float* absmax,
-                       uint16_t* h, hipStream_t stream) {
+hipError_t launch_gate(const LayerCall& c, const LayerPlan& p, const Router& rt, const void* x,
+                       const float* absmax, uint16_t* h, hipStream_t stream) {
   const int64_t n = 2 * c.F;
-  // 128 weight rows per block where that leaves blocks enough, else 64, as k_experts_few
-  // (16 tokens, 8 of 64 experts: 22.8 -> 18.1 us; one token 11.0 / 7.8)
-  const int waves = !PAIRS && ((n + 127) / 128) * std::min(c.T * c.k, c.E) >= 512 ? 8 : 4,
-            bn = 16 * waves;
+  const int bn = 16 * p.gate_waves;
   const dim3 grid((unsigned)((n + bn - 1) / bn), (unsigned)((PAIRS ? c.T * c.k : c.E) + 1));
-  const size_t lds = rows_lds(c.K, c.T, MODE);
+  const size_t lds = (size_t)layer_rows_lds(c.K, c.T, MODE == kInt8 ? 0 : MODE == kBf16 ? 2 : 4);
   auto go = [&](auto kern) {
     hipError_t e = kern.allow_lds();
     if (e != hipSuccess) return e;
-    kern.kernel<<<grid, 64 * waves, lds, stream>>>(rt, reinterpret_cast<const uint32_t*>(c.gu),
-                                                   c.gamma_gate, c.gamma_up, x, absmax, (int)n,
-                                                   (int)c.K, h);
+    kern.kernel<<<grid, 64 * p.gate_waves, lds, stream>>>(
+        rt, reinterpret_cast<const uint32_t*>(c.gu), c.gamma_gate, c.gamma_up, x, absmax, (int)n,
+        (int)c.K, h);
     return hipGetLastError();
   };
   if (c.K < 64) return go(Kernel<k_layer_gate<MODE, PAIRS, 2, kWords>>{});
@@ -510,61 +498,29 @@ hipError_t launch_gate(const LayerCall& c, const Router& rt, const void* x, cons
                   : by_depth(std::integral_constant<int, kWhole>{});
 }
 
-// Blocks of (token, rank) pairs for at most four tokens, whose waves rank a token each,
-// where they spare a thousand blocks of experts that no token takes (about 2 us; to find
-// the expert takes 1.5).  Of 2560 -> 2 x 1024, 32 blocks an expert, per expert / per pair: one
-// token, 8 of 64 experts 10.4 / 8.7 us, of 128 10.7 / 8.4, of 256 13.1 / 11.3; four tokens,
-// 8 of 64 13.8 / 12.0; but one token, 8 of 16 7.6 / 8.2, 4 of 32 7.3 / 7.7.
 template <int MODE>
-hipError_t launch_gate(const LayerCall& c, const Router& rt, const void* x, const float* absmax,
-                       uint16_t* h, hipStream_t stream) {
-  const bool pairs = c.T <= kPairTokens && (c.E - c.T * c.k) * ((2 * c.F + 63) / 64) >= 1024;
-  return pairs ? launch_gate<MODE, true>(c, rt, x, absmax, h, stream)
-               : launch_gate<MODE, false>(c, rt, x, absmax, h, stream);
+hipError_t launch_gate(const LayerCall& c, const LayerPlan& p, const Router& rt, const void* x,
+                       const float* absmax, uint16_t* h, hipStream_t stream) {
+  return p.pairs ? launch_gate<MODE, true>(c, p, rt, x, absmax, h, stream)
+                 : launch_gate<MODE, false>(c, p, rt, x, absmax, h, stream);
 }
 
 template <int RT>
-hipError_t launch_down(const LayerCall& c, const Router& rt, const uint16_t* h, hipStream_t stream) {
-  const int nchunks = (int)((c.F + 255) / 256);
-  const int topk = (int)c.k, team = std::max(1, std::min(16 / topk, (nchunks + 3) / 4));
+hipError_t launch_down(const LayerCall& c, const LayerPlan& p, const Router& rt, const uint16_t* h,
+                       hipStream_t stream) {
+  const int topk = (int)c.k;
   const dim3 grid((unsigned)((c.N + 16 * RT - 1) / (16 * RT)), (unsigned)c.T);
-  const size_t lds = (size_t)topk * few_stride((int)c.F);
+  const size_t lds = (size_t)layer_rows_lds(c.F, topk, 0);
   auto go = [&](auto kern) {
     hipError_t e = kern.allow_lds();
     if (e != hipSuccess) return e;
-    kern.kernel<<<grid, 64 * topk * team, lds, stream>>>(rt.ids, rt.weights, topk, (int)c.E, team,
-                                                         reinterpret_cast<const uint32_t*>(c.down),
-                                                         c.gamma_down, h, (int)c.N, (int)c.F, c.y);
+    kern.kernel<<<grid, 64 * topk * p.team, lds, stream>>>(rt.ids, rt.weights, topk, (int)c.E, p.team,
+                                                           reinterpret_cast<const uint32_t*>(c.down),
+                                                           c.gamma_down, h, (int)c.N, (int)c.F, c.y);
     return hipGetLastError();
   };
   if (c.F < 64) return go(Kernel<k_layer_down<RT, 4, kWords>>{});
   return c.F % 64 ? go(Kernel<k_layer_down<RT, 4, kShort>>{}) : go(Kernel<k_layer_down<RT, 4, kWhole>>{});
-}
-
-// 32 outputs per block where blocks of 16 would be more than four per CU, which
-// run at once (16 tokens, 8 of 64 experts, 1024 -> 2560: 18.1 -> 17.1 us; 3 tokens 6.4 / 6.6,
-// one 5.1 / 6.6; 64 outputs 19.5).  Blocks of one run of outputs side by side on an XCD,
-// for its L2, gained nothing (19.7).
-hipError_t launch_down_by_size(const LayerCall& c, const Router& rt, const uint16_t* h,
-                               hipStream_t stream) {
-  return (c.N + 15) / 16 * c.T > 4 * device_cus() ? launch_down<2>(c, rt, h, stream)
-                                                  : launch_down<1>(c, rt, h, stream);
-}
-
-// Step A1 in every block, or in a launch of its own before.  Its own / in the blocks,
-// bfloat16, 8 of 64 experts of 2560 -> 1024 -> 2560: one token 16.2 / 13.9 us, four 22.4 /
-// 20.8, six 27.3 / 26.6, eight 29.5 / 30.4, sixteen 39.1 / 47.0; 2 of 16 of 4096, six 36.4 / 32.3,
-// eight 41.8 / 43.1.  Rows of binary32 take LDS from other blocks: three tokens of 2560
-// (38 KB) 20.1 / 19.3, four (51 KB) 22.5 / 25.6, of 4096 three (61 KB) 26.3 / 28.1.
-bool in_blocks(const LayerCall& c, int mode) {
-  return c.T <= kRawTokens && rows_lds(c.K, c.T, mode) <= (size_t)(mode == kBf16 ? kMaxLds : 48 * 1024);
-}
-
-bool two_launches(const LayerCall& c) {
-  // the last: blocks of up to 1024 threads, fewer than 2^32 of them in a row of the grid
-  return c.T <= kTokens && c.k <= kTopK && c.E <= kLayerExperts &&
-         rows_lds(c.K, c.T, kInt8) <= (size_t)kMaxLds && rows_lds(c.F, c.k, kInt8) <= (size_t)kMaxLds &&
-         c.N < (1 << 25);
 }
 
 }  // namespace
@@ -581,21 +537,20 @@ hipError_t launch_layer(const LayerCall& c, hipStream_t stream) {
   uint16_t* h = reinterpret_cast<uint16_t*>(ws + l.h);
   int8_t* xq = reinterpret_cast<int8_t*>(ws + l.xq);
   hipError_t e;
-  if (two_launches(c)) {
+  const int raw = c.x_dtype == BL_CODES ? 0 : c.x_dtype == BL_BF16 ? 2 : 4;
+  const LayerPlan p = layer_plan(c.T, c.E, c.k, c.F, c.K, c.N, raw, device_cus());
+  if (p.two) {
     const Router rt{c.logits, (int)c.T, (int)c.E, (int)c.k, c.share, c.logits_bf16, i32(l.ids), f32(l.weights)};
-    if (c.x_dtype == BL_CODES) {
-      e = launch_gate<kInt8>(c, rt, c.x, c.absmax, h, stream);
+    if (p.own_quant) {
+      e = launch_quant(c.x, raw == 2, c.T, c.K, xq, f32(l.absmax), nullptr, stream);
+      if (e == hipSuccess) e = launch_gate<kInt8>(c, p, rt, xq, f32(l.absmax), h, stream);
     } else {
-      const int mode = c.x_dtype == BL_BF16 ? kBf16 : kF32;
-      if (in_blocks(c, mode)) {
-        e = mode == kBf16 ? launch_gate<kBf16>(c, rt, c.x, nullptr, h, stream)
-                          : launch_gate<kF32>(c, rt, c.x, nullptr, h, stream);
-      } else {
-        e = launch_quant(c.x, mode == kBf16, c.T, c.K, xq, f32(l.absmax), nullptr, stream);
-        if (e == hipSuccess) e = launch_gate<kInt8>(c, rt, xq, f32(l.absmax), h, stream);
-      }
+      e = raw == 0   ? launch_gate<kInt8>(c, p, rt, c.x, c.absmax, h, stream)
+          : raw == 2 ? launch_gate<kBf16>(c, p, rt, c.x, nullptr, h, stream)
+                     : launch_gate<kF32>(c, p, rt, c.x, nullptr, h, stream);
     }
-    return e == hipSuccess ? launch_down_by_size(c, rt, h, stream) : e;
+    if (e != hipSuccess) return e;
+    return p.down_tiles == 2 ? launch_down<2>(c, p, rt, h, stream) : launch_down<1>(c, p, rt, h, stream);
   }
   // the three calls, one after the other
   const bl_routing r{c.T, c.k, c.E, i32(l.offsets), i32(l.pairs), i32(l.slots), f32(l.weights)};
