@@ -160,6 +160,15 @@ bl_status bitlinear_experts_ffn(const void* logits, int logits_dtype, int64_t T,
                                 int64_t N, float* y, void* workspace, size_t workspace_bytes,
                                 void* stream) {
   const char* fn = "bitlinear_experts_ffn";
+  // sizes first: the workspace query answers 0 for those out of range, so that there may be none
+  if (bl_status rc = check_counts(fn, T, k, E)) return rc;
+  if (bl_status rc = check_k(fn, K)) return rc;
+  if (F < 16 || F > BITLINEAR_MAX_K || F % 16 != 0 || 2 * F * K > kMaxNK / E ||
+      T * k > kMaxTN / (2 * F))
+    return fail(BL_ERR_SHAPE, "%s: F=%lld must be a multiple of 16 in [16, %d], with E*2F*K up to 2^38 "
+                "and T*k*2F up to 2^36", fn, (long long)F, BITLINEAR_MAX_K);
+  if (N < 1 || N > kMaxN || N * F > kMaxNK / E || T * k > kMaxTN / N)
+    return fail(BL_ERR_SHAPE, "%s: N=%lld out of range", fn, (long long)N);
   if (!logits || !x || !packed_gu || !gamma_gate || !gamma_up || !packed_down || !gamma_down || !y ||
       !workspace || (x_dtype == BL_CODES && !absmax))
     return fail(BL_ERR_NULL, "%s: NULL pointer argument", fn);
@@ -169,15 +178,8 @@ bl_status bitlinear_experts_ffn(const void* logits, int logits_dtype, int64_t T,
     return fail(BL_ERR_DTYPE, "%s: unknown x_dtype %d", fn, x_dtype);
   if (x_dtype != BL_CODES && absmax)
     return fail(BL_ERR_ARG, "%s: absmax belongs to int8 codes (BL_CODES)", fn);
-  if (bl_status rc = check_counts(fn, T, k, E)) return rc;
   if (share != BL_SHARE_CHOSEN && share != BL_SHARE_ALL)
     return fail(BL_ERR_ARG, "%s: unknown share %d (BL_SHARE_CHOSEN or BL_SHARE_ALL)", fn, share);
-  if (bl_status rc = check_k(fn, K)) return rc;
-  if (bl_status rc = check_k(fn, F)) return rc;
-  if (2 * F * K > kMaxNK / E || T * k > kMaxTN / (2 * F))
-    return fail(BL_ERR_SHAPE, "%s: F=%lld out of range", fn, (long long)F);
-  if (N < 1 || N > kMaxN || N * F > kMaxNK / E || T * k > kMaxTN / N)
-    return fail(BL_ERR_SHAPE, "%s: N=%lld out of range", fn, (long long)N);
   if (!aligned(x, 16) || !aligned(packed_gu, 16) || !aligned(packed_down, 16) ||
       !aligned(workspace, 16) || !aligned(logits, logits_dtype == BL_F32 ? 4 : 2) ||
       !aligned(absmax, 4) || !aligned(gamma_gate, 4) || !aligned(gamma_up, 4) ||

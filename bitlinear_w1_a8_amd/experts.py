@@ -229,7 +229,8 @@ def experts_ffn(x, logits, k, packed_gu, gamma_gate, gamma_up, packed_down, gamm
                 share="chosen", out=None):
     """A whole routed layer, the same bits as route_experts, gated_relu2_experts
     and linear_experts one after the other; for up to 16 tokens in two launches
-    (three where more than a few are not quantised yet).
+    (three where more than a few are not quantised yet), if k <= 16, E <= 256,
+    N < 2^25, and T int8 rows of K and k of F fit 150 KiB each.
 
     x [T, K]: float32 or bfloat16, or int8 codes with their ``absmax`` float32
     [T] (quant_act, subln_quant_act, add_subln_quant_act); logits [T, E] (float32

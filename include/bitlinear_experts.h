@@ -154,8 +154,10 @@ size_t bitlinear_experts_ffn_workspace_bytes(int64_t T, int64_t E, int64_t k, in
 /* A whole routed feed-forward layer: bitlinear_route_experts of the logits,
  * bitlinear_gated_relu2_experts of the tokens and bitlinear_linear_experts of
  * its rows with the weighted sum, the same bits.  A few tokens (up to 16, with
- * k <= 16 and E <= 256) take two launches, three where more than six of them (of
- * binary32 fewer) are not quantised yet; more take the three calls' launches.
+ * k <= 16, E <= 256 and N < 2^25, and T rows of K and k rows of F int8 within 150 KiB of
+ * LDS each: 16 tokens of up to 9472, 8 experts of up to 18944) take two launches, three
+ * where more than six of them (of binary32 fewer) are not quantised yet; all others take
+ * the three calls' launches.
  *
  *   logits, logits_dtype, T, E, k, share   as bitlinear_route_experts.
  *   x           [T, K]: activations of dtype BL_F32 or BL_BF16, or (BL_CODES) step
