@@ -244,7 +244,10 @@ __global__ __launch_bounds__(1024) void k_add_subln(const Args a) {
     ms = (float)(exact / (double)K);
   }
   const float root = sqrtf(ms + a.eps_n);            // binary32, each rounded once
-  const float r = 1.0f / root;
+  float r = 1.0f / root;
+  // a mean square that is no binary32 number gives no norm, which e4m3 codes can say
+  if constexpr (F8)
+    if (!(s < (double)__builtin_inff() && ms < __builtin_inff())) r = __builtin_nanf("");
 
   uint8_t* qr = a.xq + row * K;
   if constexpr (F8) {

@@ -22,6 +22,10 @@
  * that neighbouring tokens' scales of one group are neighbours in memory.
  * Matrices: one group per block of 128 rows x 128 columns (the last ones may
  * be smaller), codes [N, K] row-major, scales [ceil(N / 128), ceil(K / 128)].
+ *
+ * A value that is NaN or infinite gets a NaN code (0x7f or 0xff), and the other
+ * codes and the scale of its group may then be any.  All outputs of a token, or of a matrix
+ * row, with a NaN code are NaN.  Groups, tokens and rows without one do not depend on it.
  */
 #ifndef BITLINEAR_F8_H
 #define BITLINEAR_F8_H

@@ -13,6 +13,7 @@
  *              or x where there is no residual;
  *   r, x_hat = as bitlinear_subln_quant_act defines them for the row `total`
  *              (exact sum of squares, r in binary32, x_hat = RN32(RN32(total * g) * r)).
+ * Whatever a row holds, the other rows' results do not depend on it.
  */
 #ifndef BITLINEAR_NORM_H
 #define BITLINEAR_NORM_H
@@ -51,6 +52,8 @@ bl_status bitlinear_add_subln_quant_act(const void* x, int x_dtype, const void* 
  *   x .. total  as bitlinear_add_subln_quant_act.
  *   xq        [T, K] e4m3 output, 16-byte aligned.
  *   scales    [ceil(K / 128), T] float32 output: scales[g * T + t].
+ * A row whose mean square is no binary32 number (a NaN or infinity in `total`, or a
+ * square sum beyond binary32's range) gets NaN for every code.
  * Errors: as bitlinear_add_subln_quant_act. */
 bl_status bitlinear_add_subln_quant_act_f8(const void* x, int x_dtype, const void* residual,
                                            int r_dtype, const float* gain, float eps_n, int64_t T,
