@@ -74,6 +74,17 @@ def _near(y, want, size, k):
 
 
 @pytest.mark.parametrize("t,n,k", SHAPES)
+def test_bfloat16_is_the_binary32_result_rounded(bl, t, n, k):
+    """The same kernels and order for either type of output; up to 16 tokens the caller's leave to
+    cut sums changes nothing."""
+    args = _cuda(*_random(t, n, k))
+    y = bl.forward_f8(*args).bfloat16()
+    assert torch.equal(bl.forward_f8(*args, dtype=torch.bfloat16), y)
+    if t <= 16:
+        assert torch.equal(bl.forward_f8(*args, dtype=torch.bfloat16, sums="cut"), y)
+
+
+@pytest.mark.parametrize("t,n,k", SHAPES)
 def test_cut_sums(bl, t, n, k):
     host = _random(t, n, k)
     args = _cuda(*host)
