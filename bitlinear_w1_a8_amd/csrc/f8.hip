@@ -12,7 +12,7 @@
 // two (its factors' exponents added) cut off, towards zero; measured on 16x16x128,
 // 16x16x32, 32x32x64 and 32x32x16 alike.  Each of the other seven loses less than 2^-13 of
 // the largest, so a sum is off by up to 7 * 2^-13 of its magnitudes' sum (seen: 2^-12.7; 4e-5
-// to 5e-5 in the norm), which is more than sums in binary32 may be.  The f16 ones at half the
+// to 5e-5 in the norm for Gaussian data), which is more than sums in binary32 may be.  The f16 ones at half the
 // rate hold every e4m3 exactly and add in binary32 (8e-8 in the norm).  So products take
 // the f16 ones, and the e4m3 ones only where the caller has asked for cut sums.
 #include <algorithm>
@@ -80,13 +80,14 @@ __device__ __forceinline__ void store4(void* y, int64_t at, int n, int N, const 
 // ------------------------------------------------------------------ few tokens
 
 // Up to 16 TT tokens against 16 RT rows per block or, not FULL, fewer, so that more CUs
-// have a block, which each take in some 24 GB/s (13 tokens, 6912 -> 2560, 12 rows 8.3 ->
-// 8.0 us; one token, 8192 -> 2000, 8 rows 7.4 -> 6.4, 8192 -> 128, 4 rows 7.0 -> 5.5).  The
-// block's waves take the blocks of K in turn and their sums meet in LDS, added in order
-// of the waves.  Every load goes straight to registers, two blocks of K ahead of its use
-// (four: 128256 rows 82 us, two: 56).  Bound by the stream of weights (one token, 2560 ->
-// 128256: 328 MB in 55 us, 6.0 TB/s; a pure read stream reaches 6.2), with few rows by what
-// a CU takes in and latency (13 tokens, 6912 -> 2560: 17.7 MB in 8.0 us).
+// have a block (13 tokens, 6912 -> 2560, 12 rows 8.3 -> 8.0 us; one token, 8192 -> 2000, 8
+// rows 7.4 -> 6.4, 8192 -> 128, 4 rows 7.0 -> 5.5).  The block's waves take the blocks of K
+// in turn and their sums meet in LDS, added in order of the waves.  Every load goes straight
+// to registers, two blocks of K ahead of its use (four: 128256 rows 82 us, two: 56).  Bound
+// by the stream of weights (one token, 2560 -> 128256: 328 MB in 55 us, 6.0 TB/s; a pure
+// read stream reaches 6.2), with few rows by latency: two blocks of K ahead per wave (13
+// tokens, 6912 -> 2560: 17.7 MB in 8.0 us, seven blocks of K per wave one after the other,
+// 62% of the wave cycles waiting).
 constexpr int kFewWaves = 8;
 constexpr int kFewAhead = 2;
 

@@ -21,25 +21,36 @@ enum F8Kernel {
 // time per block of 128 k and one for its start and end; the streaming kernel grows
 // with rows and lots of 64 tokens per CU, and a launch of it has fewer than 2^32 threads
 // (tiles always have, as T * N <= 2^36).  Fitted to graph replays of every kernel at 138
-// sizes (8 to 2048 tokens) with weights from memory; what the rule takes was 0.8%
-// behind the fastest on average, 15% at most.  Some of them, streaming / 64 x 64 / 128 x
-// 64 / 128 x 128 / 256 x 128 / 256 x 256:
+// sizes with weights from memory.  Measured again with these kernels (11 matrices, 17 to 2048
+// tokens), what the rule takes was 0.3% (binary32 outputs), 0.4% (bfloat16) and 1.7% (cut
+// sums) behind the fastest on average, and 8%, 14% and 25% (17 tokens, 28672 -> 8192) at
+// most.  Some of them, streaming / 64 x 64 / 128 x 64 / 128 x 128 / 256 x 128 / 256 x 256:
 //   full sums, binary32 outputs
-//    32 tokens, 2560 -> 6912      8.1 / 11.4 / 15.0 / 20.3 / 32.4
-//    96 tokens, 6912 -> 2560     36.2 / 22.0 / 32.6 / 48.3 / 82.5
-//   128 tokens, 5136 -> 13942    60.8 / 41.9 / 33.4 / 48.5 / 72.0
-//   256 tokens, 8192 -> 28672     353 / 181 / 159 / 143 / 125
-//   512 tokens, 28672 -> 8192     624 / 322 / 269 / 236 / 324
-//  2048 tokens, 2560 -> 6912      256 / 162 / 118 / 106 / 85.6
+//    32 tokens, 2560 -> 6912      8.2 / 11.2 / 14.9 / 20.2 / 32.3
+//    96 tokens, 6912 -> 2560     36.4 / 22.0 / 32.4 / 48.1 / 82.4
+//   128 tokens, 5136 -> 13942    81.3 / 41.7 / 33.1 / 48.2 / 71.5
+//   256 tokens, 8192 -> 28672     563 / 186 / 167 / 146 / 127
+//   512 tokens, 28672 -> 8192    1035 / 329 / 276 / 244 / 325
+//  2048 tokens, 2560 -> 6912      408 / 163 / 121 / 110 / 90.2
+//   full sums, bfloat16 outputs
+//   256 tokens, 2560 -> 6912     53.0 / 21.7 / 15.8 / 21.8 / 34.7
+//   512 tokens, 8192 -> 8192      319 / 101 / 80.2 / 64.6 / 95.4
+//  2048 tokens, 2560 -> 6912      397 / 148 / 108 / 96.2 / 79.5
 //   cut sums, bfloat16 outputs
-//    64 tokens, 8192 -> 28672     106 / 58.6 / 58.0 / 69.5 / 78.0 / 109
-//   256 tokens, 2560 -> 6912     37.7 / 17.5 / 12.8 / 17.8 / 24.6 / 36.4
-//   512 tokens, 8192 -> 8192      198 / 74.5 / 53.8 / 42.7 / 61.4 / 81.5
-//  2048 tokens, 6912 -> 2560      345 / 97.9 / 73.7 / 70.9 / 53.6 / 88.5
-//  2048 tokens, 2560 -> 6912      245 / 132 / 89.5 / 75.3 / 55.7 / 46.9
+//    64 tokens, 8192 -> 28672     146 / 56.3 / 55.4 / 68.3 / 72.0 / 106
+//   256 tokens, 2560 -> 6912     53.1 / 17.6 / 12.4 / 17.4 / 24.1 / 36.3
+//   512 tokens, 8192 -> 8192      319 / 76.4 / 55.1 / 43.4 / 61.2 / 81.3
+//  2048 tokens, 6912 -> 2560      346 / 96.2 / 73.5 / 71.1 / 54.3 / 74.7
+//  2048 tokens, 2560 -> 6912      396 / 135 / 91.6 / 76.6 / 56.9 / 46.5
 // The streaming kernel with 32 rows per block from 17 tokens on, where that leaves half the
-// CUs a block (32 tokens, 2560 -> 6912 9.9 -> 8.1, 8192 -> 28672 80.9 -> 72.9; 13 tokens, 6912
-// -> 2560 8.3 -> 11.7).
+// CUs a block (32 tokens, 2560 -> 6912 10.1 -> 8.2; 17 tokens, 28672 -> 8192 65.5 -> 54.2).
+// The border of 16 tokens is right for few rows and for up to 8 tokens, and costs large matrices
+// up to a seventh at 16 (16 rows / 32 rows per block / best tiles, binary32 outputs):
+//    16 tokens, 6912 -> 2560      8.8 / 14.5 / 21.3      2560 -> 6912      7.5 / 7.4 / 11.0
+//    16 tokens, 28672 -> 8192    59.0 / 53.8 / 81.7      8192 -> 28672    58.3 / 63.7 / 51.3
+//    16 tokens, 2560 -> 128256   81.0 / 96.4 / 76.2
+//     8 tokens, 28672 -> 8192    49.8 / 49.4 / 80.4      8192 -> 28672    48.2 / 59.4 / 50.7
+// so that 17 tokens take less time than 16 there (54.2, 51.2 and 75.4).
 inline F8Kernel f8_kernel(int64_t t, int64_t n, int64_t k, bool cut, int cus) {
   if (t <= 16) return kF8Few1;
   const int64_t lots = (t + 63) / 64;
