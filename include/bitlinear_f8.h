@@ -64,11 +64,14 @@ bl_status bitlinear_pack_weights_f8(const float* w, int64_t N, int64_t K, uint8_
 bl_status bitlinear_unpack_weights_f8(const uint8_t* codes, const float* scales, int64_t N,
                                       int64_t K, float* w, void* stream);
 
+/* Or'ed to y_dtype BL_BF16: sums may be cut, see bitlinear_forward_f8. */
+#define BL_CUT_SUMS 0x100
+
 /* y[t, n] = sum over blocks g of (x_scales[g, t] * w_scales[n / 128, g])
  *           * sum_{k in g} xq[t, k] * w[n, k].
  * Products and sums in binary32, for either type of output and any number of
- * tokens.  Sums go in an order that depends on the shape alone: the same inputs
- * give the same bits on every call.
+ * tokens.  Sums go in an order that depends on the shape and the device's number of
+ * CUs alone: the same inputs give the same bits on every call.
  *
  * With BL_CUT_SUMS (BL_BF16 | BL_CUT_SUMS as y_dtype) the caller allows matrix
  * instructions of twice the rate that keep fewer bits: of eight products of
@@ -84,7 +87,6 @@ bl_status bitlinear_unpack_weights_f8(const uint8_t* codes, const float* scales,
  *            with or without BL_CUT_SUMS.
  *   y        [T, N] output, aligned to its element.
  * Errors: BL_ERR_NULL, BL_ERR_SHAPE, BL_ERR_ALIGN, BL_ERR_DTYPE, BL_ERR_HIP. */
-#define BL_CUT_SUMS 0x100
 bl_status bitlinear_forward_f8(const uint8_t* w, const float* w_scales, const uint8_t* xq,
                                const float* x_scales, int64_t T, int64_t N, int64_t K, void* y,
                                int y_dtype, void* stream);
